@@ -164,7 +164,7 @@ def _prepare_distill(case, seed):
     st = {"s": s, "values": torch.empty(T, k, device=_DEV),
           "indices": torch.empty(T, k, dtype=torch.int32, device=_DEV),
           "counts": torch.empty(T, dtype=torch.int32, device=_DEV), "tail": None,
-          "loss": torch.empty(T, device=_DEV), "stats": torch.empty(T, 4, device=_DEV),
+          "loss": torch.empty(T, device=_DEV), "stats": torch.empty(T, 6, device=_DEV),
           "grad": None, "row_grad": None}
     tail = torch.empty(T, device=_DEV)
     for a in range(0, T, _chunk(V)):
@@ -271,40 +271,47 @@ def _plain_packet(x, k, tau):
 
 
 def _plain_distill(s, values, indices, counts, tail, tau, row_grad=None):
-    """(loss, stats, grad): grad is None without row_grad."""
+    """(loss, stats, grad): grad is None without row_grad.  Everything is taken
+    relative to the largest student logit and the largest in the packet."""
     T, V = s.shape
     k = values.shape[1]
-    none = torch.full((), -math.inf, device=s.device)
-    x = s.float() / tau
-    used = torch.arange(k, device=s.device) < counts.unsqueeze(1)
-    at = torch.where(used, indices.to(torch.int64), torch.zeros((), dtype=torch.int64,
-                                                                device=s.device))
-    slot = torch.where(used, at, torch.full_like(at, V))
-    xs = torch.where(used, torch.gather(x, 1, at), none)
-    ts = torch.where(xs > none, values / tau, none)
-    off = torch.cat([x, none.expand(T, 1)], 1).scatter_(1, slot, -math.inf)[:, :V]
-    lse_off = _lse(off)
-    lse = _lse(torch.stack([lse_off, _lse(xs)], 1))
-    lt = none.expand(T) if tail is None else torch.where(lse_off > none, tail, none)
-    lse_t = _lse(torch.stack([_lse(ts), lt], 1))
-    live = lse_t > none
     zero = torch.zeros((), device=s.device)
-    norm = torch.where(live, lse_t, zero)
+    none = torch.full((), -math.inf, device=s.device)
+    x = s.float()
+    used = torch.arange(k, device=s.device) < counts.unsqueeze(1)
+    slot = torch.where(used, indices.to(torch.int64), torch.full_like(indices, V).to(torch.int64))
+    xs = torch.where(used, torch.gather(x, 1, slot.clamp(max=V - 1)), none)
+    ts = torch.where(xs > none, values, none)
+    a = x.amax(1)
+    a = torch.where(a > none, a, zero)
+    b = ts.amax(1)
+    b = torch.where(b > none, b, zero)
+    x = (x - a.unsqueeze(1)) / tau
+    xs = (xs - a.unsqueeze(1)) / tau
+    ts = (ts - b.unsqueeze(1)) / tau
+    off = torch.cat([x, none.expand(T, 1)], 1).scatter_(1, slot, -math.inf)[:, :V]
+    l_off = _lse(off)
+    full = _lse(torch.stack([l_off, _lse(xs)], 1))
+    lt = none.expand(T) if tail is None else torch.where(l_off > none, tail - b / tau, none)
+    d = _lse(torch.stack([_lse(ts), lt], 1))
+    live = d > none
+    norm = torch.where(live, d, zero)
     p = torch.where(live.unsqueeze(1), torch.exp(ts - norm.unsqueeze(1)), zero)
     pt = torch.where(live, torch.exp(lt - norm), zero)
-    full = torch.where(live, lse, zero)
-    d = torch.where(p > 0, (ts - xs) - (norm - full).unsqueeze(1), zero)
-    dt = torch.where(pt > 0, (lt - lse_off) - (norm - full), zero)
-    loss = (p * d).sum(1) + pt * dt
-    stats = torch.stack([lse_off, lse, lse_t, pt], 1)
+    lnorm = torch.where(live, full, zero)
+    gap = norm - lnorm
+    inside = torch.where(p > 0, (ts - xs) - gap.unsqueeze(1), zero)
+    outside = torch.where(pt > 0, (lt - l_off) - gap, zero)
+    loss = (p * inside).sum(1) + pt * outside
+    stats = torch.stack([a, l_off, full, b, d, pt], 1)
     if row_grad is None:
         return loss, stats, None
     w = torch.where(live, row_grad / tau, zero)
-    has_off = lse_off > none
-    lo = torch.where(has_off, lse_off, zero)
-    a = torch.where(has_off, w * (torch.exp(lo - full) - pt), zero)
-    grad = a.unsqueeze(1) * torch.exp(off - lo.unsqueeze(1))
-    on = w.unsqueeze(1) * (torch.exp(xs - full.unsqueeze(1)) - p)
+    has_off = l_off > none
+    lo = torch.where(has_off, l_off, zero)
+    coef = torch.where(has_off, w * (torch.exp(lo - lnorm) - pt), zero)
+    grad = coef.unsqueeze(1) * torch.exp(off - lo.unsqueeze(1))
+    on = w.unsqueeze(1) * (torch.exp(xs - lnorm.unsqueeze(1)) - p)
     grad = torch.cat([grad, grad.new_zeros(T, 1)], 1).scatter_(1, slot, on)[:, :V]
     return loss, stats, grad.to(s.dtype)
 
@@ -504,7 +511,12 @@ def _exact_distill(st):
                                torch.zeros_like(pt))
             outs["loss"].append(cells.sum(1) + rest)
         if "stats" in outs:
-            outs["stats"].append(torch.stack([lse_off, lse, lse_t, pt], 1))
+            # relative to the largest logits on either side
+            top, top_t = x.amax(1) * tau, logit.amax(1) * tau
+            top, top_t = (torch.where(v > -math.inf, v, torch.zeros_like(v))
+                          for v in (top, top_t))
+            outs["stats"].append(torch.stack([top, lse_off - top / tau, lse - top / tau, top_t,
+                                              lse_t - top_t / tau, pt], 1))
         if "grad" in outs:
             share = torch.exp(outside - lse_off.unsqueeze(1)).nan_to_num(0.0)
             g = torch.where(picked, q - p, (qt - pt).unsqueeze(1) * share)
