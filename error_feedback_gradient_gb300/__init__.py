@@ -16,12 +16,23 @@ from .binding import (  # noqa: F401
     IDX_INT32,
     APPLY_MOMENTUM,
     APPLY_SGD,
+    DTYPE_BF16,
+    DTYPE_F16,
+    DTYPE_F32,
+    balance_grad,
+    balance_loss,
+    balance_loss_grad,
+    balance_workspace_size,
+    distill_grad,
+    distill_loss,
+    distill_loss_grad,
     index_codec_sizes,
     index_decode,
     index_encode,
     kernel_launches,
     library,
     library_path,
+    logits_topk,
     randk_compress,
     randk_workspace_size,
     sign_aggregate_apply,

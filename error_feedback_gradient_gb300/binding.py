@@ -20,6 +20,9 @@ IDX_INT32 = 0
 IDX_BITMAP = 1
 APPLY_SGD = 0
 APPLY_MOMENTUM = 1
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+DTYPE_F16 = 2
 
 KERNEL_TOPK_FUSED = 1
 KERNEL_SIGN = 2
@@ -99,6 +102,33 @@ _SIGNATURES = {
     "ef_packet_split": (ctypes.c_int32, [
         _c_vp, ctypes.c_int64, ctypes.c_int32, _c_i64p, _c_vp, _c_vp]),
     "ef_index_rebase": (ctypes.c_int32, [_c_vp, ctypes.c_int64, ctypes.c_int64, _c_vp]),
+    "ef_logits_topk": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+        ctypes.c_float, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "ef_distill_loss": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+        _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp]),
+    "ef_distill_grad": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+        _c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp, ctypes.c_int64, _c_vp]),
+    "ef_distill_loss_grad": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+        _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_float, _c_vp, _c_vp, _c_vp, ctypes.c_int64, _c_vp]),
+    "ef_balance_workspace_size": (ctypes.c_int32, [
+        ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _c_i64p,
+        ctypes.POINTER(ctypes.c_size_t)]),
+    "ef_balance_loss": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _c_vp,
+        ctypes.c_int32, _c_vp, ctypes.c_int32, _c_i64p, ctypes.c_float, ctypes.c_float, _c_vp,
+        _c_vp, _c_vp, _c_vp, ctypes.c_size_t, _c_vp]),
+    "ef_balance_grad": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+        _c_vp, ctypes.c_int32, _c_i64p, ctypes.c_float, ctypes.c_float, _c_vp, _c_vp, _c_vp,
+        _c_vp, ctypes.c_int64, _c_vp]),
+    "ef_balance_loss_grad": (ctypes.c_int32, [
+        _c_vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _c_vp,
+        ctypes.c_int32, _c_vp, ctypes.c_int32, _c_i64p, ctypes.c_float, ctypes.c_float, _c_vp,
+        _c_vp, _c_vp, _c_vp, _c_vp, ctypes.c_int64, _c_vp, ctypes.c_size_t, _c_vp]),
     "ef_workspace_status": (ctypes.c_int32, [
         _c_vp, _c_vp, ctypes.POINTER(ctypes.c_int32)]),
     "ef_profile_events": (ctypes.c_int32, [ctypes.c_int32, _c_vp, _c_vp]),
@@ -424,3 +454,214 @@ def index_rebase(indices: torch.Tensor, count: int, base: int, stream=None) -> N
     """ef_index_rebase: indices[:count] -= base, in place."""
     _check(library().ef_index_rebase(_ptr(indices), int(count), int(base), _stream(stream)),
            "ef_index_rebase")
+
+
+# ---------------------------------------------------------------------------
+# training losses
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(pointer, dtype code, rows, columns, row stride) of a 2-D CUDA tensor
+    whose rows are contiguous; the rows may lie any distance apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a 2-D tensor with contiguous rows")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{what}: expected float32, bfloat16 or float16")
+    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), _DTYPES[t.dtype], t.shape[0], t.shape[1], stride
+
+
+def _typed(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, what: str,
+           optional: bool = False) -> Optional[int]:
+    """Pointer of a contiguous CUDA tensor of `dtype` with `numel` elements."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{what}: missing")
+    if t.dtype != dtype or t.numel() != numel:
+        raise ValueError(f"{what}: expected {numel} elements of {dtype}, "
+                         f"got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _like(grad: torch.Tensor, logits: torch.Tensor):
+    """(pointer, row stride) of a gradient of `logits`."""
+    if grad.shape != logits.shape or grad.dtype != logits.dtype:
+        raise ValueError("grad: expected the logits' shape and type")
+    p, _, _, _, stride = _rows(grad, "grad")
+    return p, stride
+
+
+def logits_topk(logits: torch.Tensor, k: int, tau: float, out_values: Optional[torch.Tensor],
+                out_indices: Optional[torch.Tensor], out_counts: torch.Tensor,
+                out_tail: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ef_logits_topk: the k largest logits of every row as a packet
+    (``out_values`` fp32 and ``out_indices`` int32 [rows, k], ascending
+    positions; ``out_counts`` int32 [rows]) and, in ``out_tail`` fp32 [rows],
+    the log-sum-exp at temperature ``tau`` of the logits left out."""
+    p, dt, rows, vocab, stride = _rows(logits, "logits")
+    k = int(k)
+    _check(library().ef_logits_topk(
+        p, dt, rows, vocab, stride, k, float(tau),
+        _typed(out_values, torch.float32, rows * k, "out_values", k == 0),
+        _typed(out_indices, torch.int32, rows * k, "out_indices", k == 0),
+        _typed(out_counts, torch.int32, rows, "out_counts"),
+        _typed(out_tail, torch.float32, rows, "out_tail", True), _stream(stream)),
+        "ef_logits_topk")
+
+
+def _packets(rows: int, values: torch.Tensor, indices: torch.Tensor,
+             counts: Optional[torch.Tensor]):
+    """(k, pointers) of the row packets of `rows` rows."""
+    if values.dim() != 2 or values.shape[0] != rows:
+        raise ValueError("values: expected [rows, k]")
+    k = values.shape[1]
+    return (k, _typed(values, torch.float32, rows * k, "values"),
+            _typed(indices, torch.int32, rows * k, "indices"),
+            _typed(counts, torch.int32, rows, "counts", True))
+
+
+def distill_loss(logits: torch.Tensor, values: torch.Tensor, indices: torch.Tensor, tau: float,
+                 out_loss: torch.Tensor, out_stats: Optional[torch.Tensor] = None,
+                 counts: Optional[torch.Tensor] = None, tail: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """ef_distill_loss: per-row distillation loss of the student's logits
+    against a teacher's row packets; ``out_stats`` fp32 [rows, 6] is what
+    ``distill_grad`` reads."""
+    p, dt, rows, vocab, stride = _rows(logits, "logits")
+    k, v, i, c = _packets(rows, values, indices, counts)
+    f32 = torch.float32
+    _check(library().ef_distill_loss(
+        p, dt, rows, vocab, stride, k, v, i, c, _typed(tail, f32, rows, "tail", True),
+        float(tau), _typed(out_loss, f32, rows, "out_loss"),
+        _typed(out_stats, f32, rows * 6, "out_stats", True), _stream(stream)),
+        "ef_distill_loss")
+
+
+def distill_grad(logits: torch.Tensor, values: torch.Tensor, indices: torch.Tensor, tau: float,
+                 stats: torch.Tensor, grad: torch.Tensor,
+                 counts: Optional[torch.Tensor] = None,
+                 row_grad: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ef_distill_grad: gradient of sum(row_grad * loss) with respect to the
+    logits, from ``distill_loss``'s stats.  ``grad`` may be ``logits``."""
+    p, dt, rows, vocab, stride = _rows(logits, "logits")
+    k, v, i, c = _packets(rows, values, indices, counts)
+    f32 = torch.float32
+    g, gstride = _like(grad, logits)
+    _check(library().ef_distill_grad(
+        p, dt, rows, vocab, stride, k, v, i, c, float(tau),
+        _typed(stats, f32, rows * 6, "stats"), _typed(row_grad, f32, rows, "row_grad", True),
+        g, gstride, _stream(stream)), "ef_distill_grad")
+
+
+def distill_loss_grad(logits: torch.Tensor, values: torch.Tensor, indices: torch.Tensor,
+                      tau: float, out_loss: torch.Tensor, grad: torch.Tensor,
+                      counts: Optional[torch.Tensor] = None,
+                      tail: Optional[torch.Tensor] = None,
+                      row_grad: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ef_distill_loss_grad: loss and gradient in one pass over the logits.
+    ``grad`` may be ``logits``."""
+    p, dt, rows, vocab, stride = _rows(logits, "logits")
+    k, v, i, c = _packets(rows, values, indices, counts)
+    f32 = torch.float32
+    g, gstride = _like(grad, logits)
+    _check(library().ef_distill_loss_grad(
+        p, dt, rows, vocab, stride, k, v, i, c, _typed(tail, f32, rows, "tail", True),
+        float(tau), _typed(row_grad, f32, rows, "row_grad", True),
+        _typed(out_loss, f32, rows, "out_loss"), g, gstride, _stream(stream)),
+        "ef_distill_loss_grad")
+
+
+def balance_workspace_size(tokens: int, experts: int, k: int, seg_offsets: Sequence[int]) -> int:
+    out = ctypes.c_size_t(0)
+    _check(library().ef_balance_workspace_size(
+        int(tokens), int(experts), int(k), len(seg_offsets) - 1, _i64(seg_offsets),
+        ctypes.byref(out)), "ef_balance_workspace_size")
+    return int(out.value)
+
+
+def _balance_workspace(workspace, tokens, experts, k, seg_offsets, device):
+    if workspace is None:
+        workspace = torch.empty(balance_workspace_size(tokens, experts, k, seg_offsets),
+                                dtype=torch.uint8, device=device)
+    return workspace
+
+
+def _mask(mask: Optional[torch.Tensor], tokens: int) -> Optional[int]:
+    """Pointer of a uint8 (or bool) token mask."""
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return _typed(mask, torch.uint8, tokens, "mask", True)
+
+
+def _ids(ids: torch.Tensor, tokens: int):
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids: expected [tokens, k]")
+    return ids.shape[1], _typed(ids, torch.int32, ids.numel(), "ids")
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, seg_offsets: Sequence[int],
+                 alpha: float, beta: float, out_loss: torch.Tensor, out_counts: torch.Tensor,
+                 out_tokens: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ef_balance_loss: per segment of tokens the router's balance loss
+    (weight ``alpha``) plus its mean squared log-sum-exp (weight ``beta``), the
+    per-expert counts (int32 [nseg, experts]) and the tokens counted."""
+    p, dt, tokens, experts, stride = _rows(logits, "logits")
+    k, i = _ids(ids, tokens)
+    nseg = len(seg_offsets) - 1
+    ws = _balance_workspace(workspace, tokens, experts, k, seg_offsets, logits.device)
+    _check(library().ef_balance_loss(
+        p, dt, tokens, experts, stride, i, k, _mask(mask, tokens),
+        nseg, _i64(seg_offsets), float(alpha), float(beta),
+        _typed(out_loss, torch.float32, nseg, "out_loss"),
+        _typed(out_counts, torch.int32, nseg * experts, "out_counts"),
+        _typed(out_tokens, torch.int32, nseg, "out_tokens"), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)), "ef_balance_loss")
+
+
+def balance_grad(logits: torch.Tensor, k: int, seg_offsets: Sequence[int], alpha: float,
+                 beta: float, counts: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor,
+                 mask: Optional[torch.Tensor] = None, seg_grad: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """ef_balance_grad: gradient of sum(seg_grad * loss) with respect to the
+    router logits, from ``balance_loss``'s counts and token numbers (``k`` ids
+    per token).  ``grad`` may be ``logits``."""
+    p, dt, ntok, experts, stride = _rows(logits, "logits")
+    nseg = len(seg_offsets) - 1
+    g, gstride = _like(grad, logits)
+    _check(library().ef_balance_grad(
+        p, dt, ntok, experts, stride, int(k), _mask(mask, ntok),
+        nseg, _i64(seg_offsets), float(alpha), float(beta),
+        _typed(counts, torch.int32, nseg * experts, "counts"),
+        _typed(tokens, torch.int32, nseg, "tokens"),
+        _typed(seg_grad, torch.float32, nseg, "seg_grad", True), g, gstride, _stream(stream)),
+        "ef_balance_grad")
+
+
+def balance_loss_grad(logits: torch.Tensor, ids: torch.Tensor, seg_offsets: Sequence[int],
+                      alpha: float, beta: float, out_loss: torch.Tensor,
+                      out_counts: torch.Tensor, out_tokens: torch.Tensor, grad: torch.Tensor,
+                      mask: Optional[torch.Tensor] = None,
+                      seg_grad: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ef_balance_loss_grad: ``balance_loss`` and ``balance_grad`` in one call.
+    ``grad`` may be ``logits``."""
+    p, dt, tokens, experts, stride = _rows(logits, "logits")
+    k, i = _ids(ids, tokens)
+    nseg = len(seg_offsets) - 1
+    ws = _balance_workspace(workspace, tokens, experts, k, seg_offsets, logits.device)
+    g, gstride = _like(grad, logits)
+    _check(library().ef_balance_loss_grad(
+        p, dt, tokens, experts, stride, i, k, _mask(mask, tokens),
+        nseg, _i64(seg_offsets), float(alpha), float(beta),
+        _typed(seg_grad, torch.float32, nseg, "seg_grad", True),
+        _typed(out_loss, torch.float32, nseg, "out_loss"),
+        _typed(out_counts, torch.int32, nseg * experts, "out_counts"),
+        _typed(out_tokens, torch.int32, nseg, "out_tokens"), g, gstride, _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)), "ef_balance_loss_grad")

@@ -122,7 +122,7 @@ const char* ef_status_string(ef_status s) {
     case EF_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case EF_ERR_WORKERS: return "worker count out of range";
     case EF_ERR_ARG: return "invalid argument value";
-    case EF_ERR_ALIGN: return "pointer not 4-byte aligned";
+    case EF_ERR_ALIGN: return "pointer not aligned to its element type";
     case EF_ERR_ARCH: return "current device is not compute capability 10.3";
     case EF_ERR_CUDA: return "a CUDA call failed";
     case EF_ERR_DEVICE_TIMEOUT: return "device-side bounded wait ran out";

@@ -34,7 +34,12 @@
  * Numbers.  Every float is IEEE-754 binary32; every arithmetic step is a
  *   single round-to-nearest-even operation, never a fused multiply-add, in
  *   the order stated per function, so results are reproducible bit for bit.
- * Alignment.  Float / int32 / uint32 buffers must be 4-byte aligned.  The
+ *   The training losses (ef_logits_topk, ef_distill_*, ef_balance_*) use
+ *   exponentials and long sums instead: the order of their sums is fixed by
+ *   the call's sizes and alignment, so equal calls give equal bits, and the
+ *   results are the formulas' to a few units of 2^-23.
+ * Alignment.  Float / int32 / uint32 buffers must be 4-byte aligned, 16-bit
+ *   logits and gradients 2-byte aligned.  The
  *   kernels use 16-byte vector accesses where the addresses allow it and
  *   scalar accesses otherwise; results do not depend on the path taken.
  * Errors.  Every call returns an ef_status.  Argument errors are detected on
@@ -70,7 +75,7 @@ typedef int32_t ef_status;
 #define EF_ERR_WORKSPACE       6  /* workspace NULL, misaligned or too small           */
 #define EF_ERR_WORKERS         7  /* W < 1 or W > EF_MAX_WORKERS                       */
 #define EF_ERR_ARG             8  /* unknown enum value, or a non-finite scalar        */
-#define EF_ERR_ALIGN           9  /* a pointer is not 4-byte aligned                   */
+#define EF_ERR_ALIGN           9  /* a pointer is not aligned to its element type      */
 #define EF_ERR_ARCH           10  /* the current device is not compute capability 10.3 */
 #define EF_ERR_CUDA           11  /* a CUDA call failed; see ef_last_cuda_error()      */
 #define EF_ERR_DEVICE_TIMEOUT 12  /* device-side: a bounded inter-block wait ran out   */
@@ -445,6 +450,165 @@ EF_API ef_status ef_index_rebase(int32_t* indices, int64_t count, int64_t base,
 EF_API ef_status sign_aggregate_apply(int32_t W, const uint32_t* const* h_bits,
                                int64_t n, int32_t mode, float eta, float beta1,
                                float* G, float* w_or_m, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Training losses: where the gradients that the calls above compress come
+ * from.  A row is one token (or one image); logits and their gradients are
+ * [rows][row_stride] with the first `vocab` elements of a row in use, of type
+ *   EF_DTYPE_F32, EF_DTYPE_BF16 or EF_DTYPE_F16.
+ * Sums, softmax statistics and losses are fp32 whatever that type; a
+ * gradient is rounded to it once, at the end.
+ *
+ * A row packet is the per-row form of the packets above: up to `k` fp32
+ * values with int32 positions, strictly ascending, of which the first
+ * counts[row] are in use.
+ *
+ * Shared limits: 0 <= rows < 2^31, 0 <= vocab <= 2^30, row_stride >= vocab,
+ * 0 <= k <= min(vocab, EF_MAX_ROW_PACKET), 0 < tau < inf.
+ * ---------------------------------------------------------------------- */
+#define EF_DTYPE_F32  0
+#define EF_DTYPE_BF16 1
+#define EF_DTYPE_F16  2
+#define EF_MAX_ROW_PACKET 1024
+#define EF_MAX_EXPERTS 1024
+
+/* ------------------------------------------------------------------------
+ * A teacher's answer as row packets: the k largest logits of every row and
+ * the weight of all others.
+ *   S        = the k largest x[v]; ties to the lower index, NaN above +Inf,
+ *              -0 equal to +0; a logit of -Inf is never taken
+ *   count    = |S|  (less than k only where the row has fewer entries > -Inf)
+ *   values   = x[v], indices = v for v in S, ascending; unused slots 0 and -1
+ *   tail     = log sum_{v not in S} exp(x[v] / tau), -Inf for an empty sum
+ * With k = 0 the tail is the log-sum-exp of the whole row.
+ *
+ * out_values  [rows][k] fp32, out_indices [rows][k] int32 (may be NULL for
+ *             k = 0); out_counts [rows] int32; out_tail [rows] fp32 or NULL.
+ * Outputs must not overlap logits or each other.
+ * Device status: none can arise; the call takes no workspace.
+ * ---------------------------------------------------------------------- */
+EF_API ef_status ef_logits_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                int64_t row_stride, int32_t k, float tau, float* out_values,
+                                int32_t* out_indices, int32_t* out_counts, float* out_tail,
+                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * Distillation from row packets, forward and backward.
+ *
+ * s = a row of student logits, (i_j, t_j), j < count, its packet, l the
+ * packet's tail.  A student logit of -Inf masks its position: it is in
+ * neither distribution, and a packet entry there does not count.  With On
+ * the packet's live positions and Off all other live ones:
+ *   student   L = log sum_{On, Off} exp(s/tau), q_v = exp(s_v/tau - L),
+ *             L_off = log sum_Off exp(s/tau), q_off = exp(L_off - L)
+ *   teacher   D = log(sum_On exp(t_j/tau) + exp(l)), p_j = exp(t_j/tau - D),
+ *             p_off = exp(l - D); no tail given, or Off empty: the term in l
+ *             is left out (p is then a softmax over the packet alone)
+ *   loss      = sum_On p_j log(p_j / q_j) + p_off log(p_off / q_off)
+ *   d loss / d s_v = (q_v - p_v) / tau                           on On
+ *                  = (q_off - p_off) exp(s_v/tau - L_off) / tau  on Off
+ *                  = 0                                           masked
+ * A row whose teacher has nothing left (D = -Inf: count 0 and no tail, or
+ * everything masked) has loss 0 and gradient 0.  The sum over Off is taken
+ * over Off itself, never as a difference, so a packet that holds nearly all
+ * the mass loses no digits.  +Inf or NaN in the row's s, t or l gives a NaN
+ * loss and gradient (0 or NaN at masked positions).
+ *
+ * ef_distill_loss       out_loss [rows] fp32, and optionally out_stats
+ *                       [rows][6] fp32 = (a, L_off - a/tau, L - a/tau, b,
+ *                       D - b/tau, p_off), which ef_distill_grad reads; a is
+ *                       the row's largest student logit, b the largest live
+ *                       packet value (0 where there is none): logits far from
+ *                       0 lose no digits.  p_off = 0 where D = -Inf.
+ * ef_distill_grad       grad[row][v] = row_grad[row] * d loss / d s_v from
+ *                       the same logits and packet and those stats.
+ * ef_distill_loss_grad  both in one pass over the logits, for a caller that
+ *                       knows row_grad beforehand (weights, a mean).
+ *
+ * values, indices  [rows][k] the packets; counts [rows] int32 or NULL (all k
+ *                  in use); a count above k reads as k, below 0 as 0.
+ * tail             [rows] fp32 or NULL.
+ * row_grad         [rows] fp32 or NULL (all 1).  A row_grad of 0 gives a
+ *                  gradient of +0 whatever the row holds.
+ * grad             [rows][grad_stride] of the logits' type; may be the logits
+ *                  themselves (same address and stride), else no overlap.
+ *                  Only its first `vocab` elements per row are written.
+ * Device status: none; the calls take no workspace.  A packet whose indices
+ * are not strictly ascending in [0, vocab) is never followed out of bounds:
+ * its row's loss, stats and gradient are NaN.
+ * ---------------------------------------------------------------------- */
+EF_API ef_status ef_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                 int64_t row_stride, int32_t k, const float* values,
+                                 const int32_t* indices, const int32_t* counts,
+                                 const float* tail, float tau, float* out_loss,
+                                 float* out_stats, void* stream);
+EF_API ef_status ef_distill_grad(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                 int64_t row_stride, int32_t k, const float* values,
+                                 const int32_t* indices, const int32_t* counts, float tau,
+                                 const float* stats, const float* row_grad, void* grad,
+                                 int64_t grad_stride, void* stream);
+EF_API ef_status ef_distill_loss_grad(const void* logits, int32_t dtype, int64_t rows,
+                                      int64_t vocab, int64_t row_stride, int32_t k,
+                                      const float* values, const int32_t* indices,
+                                      const int32_t* counts, const float* tail, float tau,
+                                      const float* row_grad, float* out_loss, void* grad,
+                                      int64_t grad_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A router's balance loss and per-expert counts, forward and backward.
+ *
+ * z = [tokens][experts] router logits (row_stride between tokens), ids =
+ * [tokens][k] int32 the experts each token was sent to; an id outside
+ * [0, experts) counts for none (a dropped assignment).  A token with
+ * mask[t] = 0 is padding: it counts nowhere and its gradient is 0.  Per
+ * segment (a sequence, or the whole batch), over its n unmasked tokens:
+ *   c_e  = number of ids equal to e           f_e = experts * c_e / (k * n)
+ *   p_te = softmax_e(z_t)                     L_t = log sum_e exp(z_te)
+ *   loss = alpha * sum_e f_e * mean_t p_te + beta * mean_t L_t^2   (0 if n = 0)
+ *   d loss / d z_te = p_te (alpha (f_e - sum_e' f_e' p_te') + 2 beta L_t) / n
+ * (the counts have no derivative).  A logit of -Inf masks its expert; a
+ * token whose logits are all -Inf counts in n and c but adds nothing to the
+ * sums, and its gradient is 0.
+ *
+ * ef_balance_loss       out_loss [nseg] fp32, out_counts [nseg][experts]
+ *                       int32 (c), out_tokens [nseg] int32 (n).
+ * ef_balance_grad       grad = seg_grad[segment] * d loss / d z from those
+ *                       counts and token numbers.
+ * ef_balance_loss_grad  both, for a caller that knows seg_grad beforehand.
+ *
+ * tokens        0 .. 2^31 - 1; experts 1 .. EF_MAX_EXPERTS; k 1 .. EF_MAX_EXPERTS.
+ * h_seg_offsets [nseg + 1] host, rising from 0 to tokens; segments may be empty.
+ * mask          [tokens] uint8 or NULL (none masked).
+ * seg_grad      [nseg] fp32 or NULL (all 1).
+ * grad          [tokens][grad_stride] of the logits' type; may be the logits
+ *               themselves (same address and stride), else no overlap.
+ * workspace     >= ef_balance_workspace_size() bytes, 256-byte aligned.
+ * Device status: none beyond EF_OK.
+ * ---------------------------------------------------------------------- */
+EF_API ef_status ef_balance_workspace_size(int64_t tokens, int32_t experts, int32_t k,
+                                           int32_t nseg, const int64_t* h_seg_offsets,
+                                           size_t* bytes);
+EF_API ef_status ef_balance_loss(const void* logits, int32_t dtype, int64_t tokens,
+                                 int32_t experts, int64_t row_stride, const int32_t* ids,
+                                 int32_t k, const uint8_t* mask, int32_t nseg,
+                                 const int64_t* h_seg_offsets, float alpha, float beta,
+                                 float* out_loss, int32_t* out_counts, int32_t* out_tokens,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+EF_API ef_status ef_balance_grad(const void* logits, int32_t dtype, int64_t tokens,
+                                 int32_t experts, int64_t row_stride, int32_t k,
+                                 const uint8_t* mask, int32_t nseg,
+                                 const int64_t* h_seg_offsets, float alpha, float beta,
+                                 const int32_t* counts, const int32_t* token_counts,
+                                 const float* seg_grad, void* grad, int64_t grad_stride,
+                                 void* stream);
+EF_API ef_status ef_balance_loss_grad(const void* logits, int32_t dtype, int64_t tokens,
+                                      int32_t experts, int64_t row_stride, const int32_t* ids,
+                                      int32_t k, const uint8_t* mask, int32_t nseg,
+                                      const int64_t* h_seg_offsets, float alpha, float beta,
+                                      const float* seg_grad, float* out_loss,
+                                      int32_t* out_counts, int32_t* out_tokens, void* grad,
+                                      int64_t grad_stride, void* workspace,
+                                      size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Device-side status of the last call that used `workspace`: synchronises
