@@ -43,6 +43,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// log2 by the same unit: absolute error at most 2^-22 near 1, 2^-22 relative
+// elsewhere.
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // exp(a - b) for log-domain a, b; 0 where a is -Inf (b may be too).
 __device__ __forceinline__ float exp_diff(float a, float b) {
   return a == kNegInf ? 0.0f : expf(a - b);
@@ -89,6 +97,189 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
   v = warp_sum(lane_id() < (blockDim.x >> 5) ? scratch[lane_id()] : 0.0f);
   __syncthreads();
   return v;
+}
+
+// ---------------------------------------------------------------------------
+// Rows in 16-byte slots.
+//
+// A row starts anywhere (an odd vocabulary in 16-bit logits), so its vectors
+// are the aligned 16-byte blocks that lie wholly inside it: `head` elements,
+// then `slots` blocks of N elements, then `tail` elements.  The at most
+// 2 (N - 1) elements at the two ends are read and written one at a time, one
+// thread each, so nothing outside the row is touched.
+// ---------------------------------------------------------------------------
+
+struct RowShape {
+  int head, slots, edge;  // edge = head + tail
+};
+
+template <typename T>
+struct Slot {
+  static constexpr int N = 16 / (int)sizeof(T);
+
+  static __device__ __forceinline__ RowShape shape(const T* row, int vocab) {
+    const int phase = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    RowShape r;
+    r.head = min((N - phase) & (N - 1), vocab);
+    r.slots = (vocab - r.head) / N;
+    r.edge = vocab - r.slots * N;
+    return r;
+  }
+  // position of edge element i (i < edge)
+  static __device__ __forceinline__ int edge_at(const RowShape& r, int i) {
+    return i < r.head ? i : r.slots * N + i;
+  }
+  static __device__ __forceinline__ uint4 load(const T* row, const RowShape& r, int slot) {
+    return __ldcs(reinterpret_cast<const uint4*>(row + r.head) + slot);
+  }
+  static __device__ __forceinline__ uint4 pack(const float2 (&f)[N / 2]);
+  static __device__ __forceinline__ void unpack(const uint4& r, float2 (&f)[N / 2]);
+  static __device__ __forceinline__ uint4 none();  // -Inf everywhere
+  static __device__ __forceinline__ float max(const uint4& r);
+  // replaces the elements whose bit is set by -Inf
+  static __device__ __forceinline__ void mask(uint4& r, uint32_t bits);
+};
+
+template <>
+__device__ __forceinline__ void Slot<float>::mask(uint4& r, uint32_t bits) {
+  if (bits & 1u) r.x = 0xFF800000u;
+  if (bits & 2u) r.y = 0xFF800000u;
+  if (bits & 4u) r.z = 0xFF800000u;
+  if (bits & 8u) r.w = 0xFF800000u;
+}
+// two 16-bit elements of a word
+__device__ __forceinline__ uint32_t mask_pair(uint32_t w, uint32_t bits, uint32_t neg_inf) {
+  const uint32_t sel = (bits & 1u ? 0xFFFFu : 0u) | (bits & 2u ? 0xFFFF0000u : 0u);
+  return (w & ~sel) | (neg_inf & sel);
+}
+template <>
+__device__ __forceinline__ void Slot<__nv_bfloat16>::mask(uint4& r, uint32_t bits) {
+  r.x = mask_pair(r.x, bits, 0xFF80FF80u);
+  r.y = mask_pair(r.y, bits >> 2, 0xFF80FF80u);
+  r.z = mask_pair(r.z, bits >> 4, 0xFF80FF80u);
+  r.w = mask_pair(r.w, bits >> 6, 0xFF80FF80u);
+}
+template <>
+__device__ __forceinline__ void Slot<__half>::mask(uint4& r, uint32_t bits) {
+  r.x = mask_pair(r.x, bits, 0xFC00FC00u);
+  r.y = mask_pair(r.y, bits >> 2, 0xFC00FC00u);
+  r.z = mask_pair(r.z, bits >> 4, 0xFC00FC00u);
+  r.w = mask_pair(r.w, bits >> 6, 0xFC00FC00u);
+}
+
+template <>
+__device__ __forceinline__ uint4 Slot<float>::none() {
+  return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+}
+template <>
+__device__ __forceinline__ uint4 Slot<__nv_bfloat16>::none() {
+  return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+}
+template <>
+__device__ __forceinline__ uint4 Slot<__half>::none() {
+  return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+}
+
+template <>
+__device__ __forceinline__ void Slot<float>::unpack(const uint4& r, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+  f[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+template <>
+__device__ __forceinline__ void Slot<__nv_bfloat16>::unpack(const uint4& r, float2 (&f)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ void Slot<__half>::unpack(const uint4& r, float2 (&f)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __half22float2(reinterpret_cast<const __half2&>(w[i]));
+}
+
+template <>
+__device__ __forceinline__ uint4 Slot<float>::pack(const float2 (&f)[2]) {
+  return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                    __float_as_uint(f[1].y));
+}
+template <>
+__device__ __forceinline__ uint4 Slot<__nv_bfloat16>::pack(const float2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __float22bfloat162_rn(f[i]);
+    w[i] = reinterpret_cast<const uint32_t&>(p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 Slot<__half>::pack(const float2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __float22half2_rn(f[i]);
+    w[i] = reinterpret_cast<const uint32_t&>(p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Keeps the compiler from carrying a slot's unpacked elements, twice the
+// registers of the slot itself, from one pass over it to the next.
+__device__ __forceinline__ void forget(uint4& r) {
+  asm volatile("" : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w));
+}
+
+// Two fp32 operations in one instruction, each rounded as the scalar one.
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 bits_pair(unsigned long long a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(r);
+}
+
+// Largest element, NaN ignored (16-bit types: two at a time).
+template <>
+__device__ __forceinline__ float Slot<float>::max(const uint4& r) {
+  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+template <typename P>
+__device__ __forceinline__ P max_pairs(const uint4& r) {
+  return __hmax2(__hmax2(reinterpret_cast<const P&>(r.x), reinterpret_cast<const P&>(r.y)),
+                 __hmax2(reinterpret_cast<const P&>(r.z), reinterpret_cast<const P&>(r.w)));
+}
+template <>
+__device__ __forceinline__ float Slot<__nv_bfloat16>::max(const uint4& r) {
+  const float2 p = __bfloat1622float2(max_pairs<__nv_bfloat162>(r));
+  return fmaxf(p.x, p.y);
+}
+template <>
+__device__ __forceinline__ float Slot<__half>::max(const uint4& r) {
+  const float2 p = __half22float2(max_pairs<__half2>(r));
+  return fmaxf(p.x, p.y);
 }
 
 // ---------------------------------------------------------------------------
