@@ -32,6 +32,8 @@ struct DistillArgs {
   int64_t grad_stride;
 };
 
+constexpr int kMaxCluster = 8;  // CTAs that share a row
+
 // What a warp (then a CTA) of a row knows after reading its share; the sums
 // are relative to the maxima beside them.
 struct Part {
@@ -68,26 +70,23 @@ __device__ __forceinline__ float lanes_max(float v, int width) {
 }
 
 // 2^((x - ref) c - k2) of a slot's elements.  The difference is taken before
-// the product: exact enough wherever the row lies, for one more paired
-// addition per two elements.
+// the product, so it does not matter how far from 0 the row lies.
 template <typename T>
 __device__ __forceinline__ void exp2_slot(const uint4& raw, float ref, float c, float k2,
                                           float2 (&f)[Slot<T>::N / 2]) {
-  Slot<T>::unpack(raw, f);
-  const float2 r2 = make_float2(-ref, -ref), c2 = make_float2(c, c), k = make_float2(-k2, -k2);
+  const float2 c2 = make_float2(c, c), k = make_float2(-k2, -k2);
+  Slot<T>::add(raw, -ref, f);
 #pragma unroll
   for (int i = 0; i < Slot<T>::N / 2; ++i) {
-    f[i] = fma2(add2(f[i], r2), c2, k);
+    f[i] = fma2(f[i], c2, k);
     f[i].x = exp2_fast(f[i].x);
     f[i].y = exp2_fast(f[i].y);
   }
 }
 template <typename T>
-__device__ __forceinline__ float sum_slot(const float2 (&f)[Slot<T>::N / 2]) {
-  float2 s = f[0];
+__device__ __forceinline__ void sum_slot(const float2 (&f)[Slot<T>::N / 2], float2& sum) {
 #pragma unroll
-  for (int i = 1; i < Slot<T>::N / 2; ++i) s = add2(s, f[i]);
-  return s.x + s.y;
+  for (int i = 0; i < Slot<T>::N / 2; ++i) sum = add2(sum, f[i]);
 }
 
 // What a sum against the reference of maximum m is multiplied by to stand
@@ -306,7 +305,9 @@ __global__ void __launch_bounds__(THREADS, 2)
       const uint32_t bits = mask[local * N >> 5] >> (local * N & 31) & ((1u << N) - 1u);
       if (c0 + local >= hi) S::mask(raw[v], ~0u);
       else if (bits != 0) S::mask(raw[v], bits);
-      m = fmaxf(m, S::max(raw[v]));
+      SlotMax<T> slot_max;
+      slot_max.add(raw[v]);
+      m = fmaxf(m, slot_max.get());
     }
     m = warp_max(m);
     const float ref = finite_ref(m);
@@ -318,7 +319,9 @@ __global__ void __launch_bounds__(THREADS, 2)
       float2 f[N / 2];
       forget(raw[v]);
       exp2_slot<T>(raw[v], ref, c, 0.0f, f);
-      s += sum_slot<T>(f);
+      float2 sum = make_float2(0.0f, 0.0f);
+      sum_slot<T>(f, sum);
+      s += sum.x + sum.y;
     }
     c0 += kCap;
     if (c0 >= hi) break;
@@ -414,79 +417,425 @@ __global__ void __launch_bounds__(THREADS, 2)
 }
 
 // ---------------------------------------------------------------------------
-// Rows that fit a cluster's registers (and all gradients taken alone, where a
-// row is cut into shares that need nothing of one another): a persistent grid
-// in which every group of GROUP threads (a warp, or a CTA) takes one row, or
-// one CTA's share of it, after another, and the next one's logits and packet
-// travel to shared memory while the current one is worked on.  A row is read
-// once and its gradient written once.
+// Rows that fit the registers of a CTA or a cluster of CTAs, and all gradients
+// taken alone (where a row is cut into shares that need nothing of one
+// another): a persistent grid in which every CTA takes one row, or its share of
+// it, after another.  A row is read once and its gradient written once.
 //
-// A row's critical path (gather, reductions, logarithms) is microseconds long,
-// much longer than its share of the memory's time, so the loads of the next
-// row are in flight during all of it.  A group takes its row from shared
-// memory to registers at once, each thread the slots that it also fetches
-// for the next row: one buffer per group is enough.
-//
-// The packet: one thread per entry takes the student's logit out of the
-// buffer and leaves -Inf there, before anyone reads the row.  The gradient is
-// first written as if no position were in the packet; after a barrier the
-// entries' threads overwrite theirs.
-//
-// Code size counts here: with the entries handled where their elements lie,
-// in the unrolled loops, the kernel stalled on instruction fetches (8.3 of 18
-// cycles per issue) and took 290 us on 4096 rows of 30522 bf16 logits.
+// The last warp of a CTA (the row warp) does everything that is done once per
+// row; the others hold the row in registers and do what is done once per
+// element.  The row warp
+//   - has the next row copied to shared memory as soon as the current one is
+//     in registers, so a copy is under way during all of a row's steps;
+//   - takes the student's logits at the packet's positions out of the buffer
+//     and leaves -Inf there, and sums the packet's side;
+//   - joins the warps' sums (and the cluster's), takes the logarithms;
+//   - writes the gradient at the packet's positions and at the row's ends
+//     (the elements outside whole 16-byte blocks), after the others have
+//     written the row as if no position were in the packet.
+// Measured on 4096 rows of 30522 bf16 logits, k 64 (floor 75 us), as one CTA's
+// steps: all threads doing everything 133 us, of 16.5 k cycles a row 3.3 k the
+// issue of the copies, 2.0 k the packet's gather, 1.4 k its sums, 2.1 k joins
+// and logarithms, each with the other warps waiting.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
+enum RowBarrier { kReady = 1, kFree, kParts, kRowDone, kStored };
 
-// Shared memory of one group, in bytes: the row buffer, the row's ends, two
-// packets (indices, values) and the current one's logits on both sides.
+// Shared memory in bytes: the row buffer, two packets (indices, values) and
+// both sides' logits at their positions.
 __host__ __device__ constexpr size_t stream_smem(int cap, int kpad) {
-  return (size_t)cap * 16 + 64 + (size_t)kpad * 24;
+  return (size_t)cap * 16 + (size_t)kpad * 32;
 }
 
-template <typename T, int GROUP, int NV, bool LOSS, bool GRAD, bool SAME>
-__global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128 ? 128 : GROUP))
+template <typename T, int WARPS, int NV, bool LOSS, bool GRAD, bool SAME>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     distill_stream(DistillArgs a, int per, int cluster, int shares, int64_t items, int kpad) {
   using S = Slot<T>;
   constexpr int N = S::N;
-  constexpr int kThreads = GROUP < 128 ? 128 : GROUP;
-  constexpr int kGroups = kThreads / GROUP;
-  constexpr int kWarps = GROUP / 32;
-  constexpr int kCap = GROUP * NV;
+  constexpr int kThreads = WARPS * 32;
+  constexpr int kWorkers = WARPS - 1;
+  constexpr int kLanes = kWorkers * 32;  // threads that hold the row
+  constexpr int kCap = kLanes * NV;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Part parts[kThreads / 32], whole[2];
-  __shared__ Row row_sh;
-  const int group = (int)threadIdx.x / GROUP, tid = (int)threadIdx.x % GROUP;
-  const int lane = tid & 31, warp = tid >> 5;
-  unsigned char* base = smem + (size_t)group * stream_smem(kCap, kpad);
+  // [kWorkers] is the row warp's own (the row's ends)
+  __shared__ float part_m[32], part_s[32];
+  __shared__ Part peers[2][kMaxCluster];
+  __shared__ Row row_sh[2];
+  struct Info {
+    int held;
+    uint4* out;
+  };
+  __shared__ Info info_sh[2];
+  __shared__ __align__(8) uint64_t full, peer;
+  uint4* buf = reinterpret_cast<uint4*>(smem);
+  float* words = reinterpret_cast<float*>(smem + (size_t)kCap * 16);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = a.c;
+  const int64_t first = blockIdx.x / cluster, step = gridDim.x / cluster;
+
+  if (warp == kWorkers) {
+    if (lane == 0) {
+      mbar_init(&full, 1);
+      mbar_init(&peer, cluster);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_bulk();
+  } else if (LOSS) {
+    // slots past a row's share read as -Inf; `held` varies by one with a row's
+    // place in its blocks, so the last of them is written again for each row
+#pragma unroll
+    for (int v = 0; v < NV; ++v) buf[v * kLanes + tid] = S::none();
+    fence_bulk();
+  }
+  if (cluster > 1) cg::this_cluster().sync();
+  else __syncthreads();
+  pdl_wait();
+
+  if (warp < kWorkers) {
+    int turn = 0;
+    for (int64_t item = first; item < items; item += step, turn ^= 1) {
+      bar_sync(kReady, kThreads);
+      const Info info = info_sh[turn];
+      uint4 raw[NV];
+      SlotMax<T> slot_max;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        raw[v] = buf[v * kLanes + tid];
+        if (LOSS) slot_max.add(raw[v]);
+        forget(raw[v]);
+      }
+      bar_arrive(kFree, kThreads);
+      if (LOSS) {
+        const float m = warp_max(slot_max.get()), ref = finite_ref(m);
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          float2 f[N / 2];
+          exp2_slot<T>(raw[v], ref, c, 0.0f, f);
+          sum_slot<T>(f, sum);
+          forget(raw[v]);
+        }
+        const float s = warp_sum(sum.x + sum.y);
+        if (lane == 0) {
+          part_m[warp] = m;
+          part_s[warp] = s;
+        }
+        __syncwarp();
+        bar_arrive(kParts, kThreads);
+        if (GRAD) bar_sync(kRowDone, kThreads);
+      }
+      if (GRAD) {
+        const float ref = row_sh[turn].ref, k2 = row_sh[turn].k2;
+        const bool dead = row_sh[turn].dead;
+        const float coef = dead ? 0.0f : row_sh[turn].coef;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int q = v * kLanes + tid;
+          if (q >= info.held) continue;
+          float2 f[N / 2];
+          exp2_slot<T>(raw[v], ref, c, k2, f);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) f[e] = mul2(f[e], make_float2(coef, coef));
+          const uint4 o = dead ? make_uint4(0, 0, 0, 0) : S::pack(f);
+          if (SAME) {
+            __stcs(info.out + q, o);
+          } else {
+            union {
+              uint4 v;
+              T e[N];
+            } u;
+            u.v = o;
+#pragma unroll
+            for (int e = 0; e < N; ++e) reinterpret_cast<T*>(info.out)[q * N + e] = u.e[e];
+          }
+        }
+        __syncwarp();
+        bar_arrive(kStored, kThreads);
+      }
+    }
+    if (cluster > 1) cg::this_cluster().sync();
+    return;
+  }
+
+  // ------------------------------------------------------------------ row warp
+  const int vocab = a.vocab;
+  const int cl_rank = LOSS ? (int)(blockIdx.x % cluster) : 0;
+  // what is known of an item before it is worked on
+  struct Next {
+    int64_t row;
+    RowShape shape;
+    int lo, held, rank;  // its slots are [lo, lo + held)
+    int count;           // as loaded, like the following: a conversion would wait
+    float row_grad, tail;
+    T end;
+  };
+  const auto describe = [&](int64_t item) {
+    Next nx;
+    nx.row = LOSS ? item : item / shares;
+    nx.rank = LOSS ? cl_rank : (int)(item - nx.row * shares);
+    const T* x = static_cast<const T*>(a.logits) + nx.row * a.stride;
+    nx.shape = S::shape(x, vocab);
+    nx.lo = (int)min((int64_t)nx.rank * per, (int64_t)nx.shape.slots);
+    nx.held = min(per, nx.shape.slots - nx.lo);
+    nx.count = a.counts ? a.counts[nx.row] : a.k;
+    nx.row_grad = GRAD && a.row_grad ? a.row_grad[nx.row] : 1.0f;
+    nx.tail = LOSS && a.tail ? a.tail[nx.row] : 0.0f;
+    if (nx.rank == 0 && lane < nx.shape.edge) nx.end = x[S::edge_at(nx.shape, lane)];
+    return nx;
+  };
+  bool lost = false;  // a wait ran out: every row from there on is NaN
+  const auto start_copy = [&](const Next& nx) {
+    if (lane == 0 && !lost) {
+      const T* x = static_cast<const T*>(a.logits) + nx.row * a.stride + nx.shape.head;
+      mbar_expect(&full, (uint32_t)nx.held * 16);
+      if (nx.held > 0)
+        bulk_copy(buf, reinterpret_cast<const uint4*>(x) + nx.lo, (uint32_t)nx.held * 16, &full);
+    }
+  };
+  const auto packet_at = [&](int turn) { return words + turn * 4 * kpad; };
+  const auto start_packet = [&](const Next& nx, int turn) {
+    float* p = packet_at(turn);
+    for (int j = lane; j < a.k; j += 32) {
+      copy_async4(p + j, a.indices + nx.row * a.k + j);
+      copy_async4(p + kpad + j, a.values + nx.row * a.k + j);
+    }
+  };
+
+  uint32_t phase = 0, peer_phase = 0;
+  int turn = 0, side = 0;
+  // row being prepared
+  Part on;
+  bool bad;
+  float end, w;
+  int n;
+  // waits for a row and its packet, takes the packet's logits out
+  const auto prepare = [&](const Next& me, int turn) {
+    float* p = packet_at(turn);
+    const int32_t* idx = reinterpret_cast<const int32_t*>(p);
+    const float* val = p + kpad;
+    float *sx = p + 2 * kpad, *tx = p + 3 * kpad;
+    n = min(max(me.count, 0), a.k);
+    w = GRAD ? me.row_grad * a.inv_tau : 0.0f;
+    end = me.rank == 0 && lane < me.shape.edge ? to_f32(me.end) : kNegInf;
+    copy_async_wait();
+    if (!lost && !mbar_wait(&full, phase)) lost = true;
+    phase ^= 1;
+    lost = __any_sync(kFull, lost);
+    bad = lost;
+    on = no_part();
+    if (LOSS && lane == 0 && me.held < per) buf[me.held] = S::none();
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane;
+      int e = -1;  // the entry's place among the row's ends
+      float s = kNegInf;
+      if (j < n) {
+        const int i = idx[j], before = j > 0 ? idx[j - 1] : -1;
+        const int pos = i - me.shape.head, q = pos - me.lo * N;
+        if (i <= before || i < 0 || i >= vocab) {
+          bad = true;
+        } else if (pos < 0 || pos >= me.shape.slots * N) {
+          if (me.rank == 0) e = pos < 0 ? i : i - me.shape.slots * N;
+        } else if (q >= 0 && q < me.held * N) {
+          T* at = reinterpret_cast<T*>(buf) + q;
+          s = to_f32(*at);
+          if (LOSS) *at = from_f32<T>(kNegInf);
+        }
+      }
+      if (__any_sync(kFull, e >= 0)) {
+        const float at_end = __shfl_sync(kFull, end, e & 31);
+        if (e >= 0) s = at_end;
+        if (LOSS) {
+          const unsigned gone = __reduce_or_sync(kFull, e >= 0 ? 1u << e : 0u);
+          if (gone >> lane & 1u) end = kNegInf;
+        }
+      }
+      if (j < n) {
+        const float t = s == kNegInf ? kNegInf : val[j];
+        sx[j] = s;
+        tx[j] = t;
+        on.m_s = fmaxf(on.m_s, s);
+        on.m_t = fmaxf(on.m_t, t);
+      }
+    }
+    bad = __any_sync(kFull, bad);
+    if (GRAD && lane == 0) {
+      T* g = static_cast<T*>(a.grad) + me.row * a.grad_stride + me.shape.head;
+      info_sh[turn] = Info{me.held, reinterpret_cast<uint4*>(g) + me.lo};
+      if (!SAME) info_sh[turn].out = reinterpret_cast<uint4*>(g + (int64_t)me.lo * N);
+    }
+  };
+  // the gradient at the packet's positions and the row's ends
+  const auto finish_grad = [&](const Next& me, int turn, const Row& r, int n, float end) {
+    T* g = static_cast<T*>(a.grad) + me.row * a.grad_stride;
+    const float* p = packet_at(turn);
+    const int32_t* idx = reinterpret_cast<const int32_t*>(p);
+    const float *sx = p + 2 * kpad, *tx = p + 3 * kpad;
+    if (me.rank == 0 && lane < me.shape.edge) {
+      const float f = r.dead ? 0.0f : r.coef * exp2_fast(fmaf(end - r.ref, c, -r.k2));
+      g[S::edge_at(me.shape, lane)] = from_f32<T>(f);
+    }
+    __syncwarp();
+    if (!r.dead)
+      for (int j = lane; j < n; j += 32)
+        if (sx[j] != kNegInf) g[idx[j]] = from_f32<T>(grad_on(r, c, sx[j], tx[j]));
+  };
+
+  if (first >= items) {
+    if (cluster > 1) cg::this_cluster().sync();
+    return;
+  }
+  Next me = describe(first);
+  start_copy(me);
+  start_packet(me, 0);
+  prepare(me, 0);
+  Row r;
+  Next last;        // the row before, whose gradient is not finished
+  Row last_r;
+  int last_n = 0;
+  float last_end = 0.0f;
+  const float nan = __int_as_float(0x7FFFFFFF);
+  for (int64_t item = first; item < items; item += step, turn ^= 1) {
+    if (!LOSS) {
+      r = stored_row(a, me.row, w);
+      if (bad) r.coef = nan;
+      r.dead = w == 0.0f || (r.dead && !bad);
+      if (lane == 0) row_sh[turn] = r;
+    }
+    __syncwarp();
+    if (GRAD && item != first) bar_sync(kStored, kThreads);
+    bar_sync(kReady, kThreads);
+    if (GRAD && item != first) finish_grad(last, turn ^ 1, last_r, last_n, last_end);
+    __syncwarp();
+    const bool more = item + step < items;
+    Next nx;
+    if (more) {
+      nx = describe(item + step);
+      __syncwarp();
+      start_packet(nx, turn ^ 1);
+    }
+    __syncwarp();
+    bar_sync(kFree, kThreads);
+    if (more) {
+      fence_bulk();
+      __syncwarp();
+      start_copy(nx);
+      __syncwarp();
+    }
+    if (LOSS) {
+      // the packet's sums and the row's ends, while the others sum the row
+      const float* p = packet_at(turn);
+      const float *sx = p + 2 * kpad, *tx = p + 3 * kpad;
+      on.m_s = warp_max(on.m_s);
+      on.m_t = warp_max(on.m_t);
+      const float rs = finite_ref(on.m_s), rt = finite_ref(on.m_t);
+      for (int j = lane; j < n; j += 32) {
+        const float y = tx[j] - rt, z = sx[j] - rs;
+        const float e = exp2_fast(y * c);
+        on.s_s += exp2_fast(z * c);
+        on.s_t += e;
+        if (e != 0.0f) on.u += e * kUnit * (y - z);
+      }
+      on.s_s = warp_sum(on.s_s);
+      on.s_t = warp_sum(on.s_t);
+      on.u = warp_sum(on.u);
+      const float m_end = warp_max(end);
+      const float s_end = warp_sum(exp2_fast((end - finite_ref(m_end)) * c));
+      bar_sync(kParts, kThreads);
+      const float mw = lane < kWorkers ? part_m[lane] : lane == kWorkers ? m_end : kNegInf;
+      const float sw = lane < kWorkers ? part_s[lane] : lane == kWorkers ? s_end : 0.0f;
+      on.m_off = warp_max(mw);
+      on.s_off = warp_sum(sw * rescale(mw, on.m_off, c));
+      if (cluster > 1 && !bad) {
+        if (lane < cluster) {
+          *cg::this_cluster().map_shared_rank(&peers[side][cl_rank], lane) = on;
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                       : "=r"(at)
+                       : "r"(smem_addr(&peer)), "r"(lane));
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at)
+                       : "memory");
+        }
+        __syncwarp();
+        if (!mbar_wait(&peer, peer_phase)) lost = true;
+        lost = __any_sync(kFull, lost);
+        peer_phase ^= 1;
+        on = join(lane < cluster ? peers[side][lane] : no_part(), cluster, c);
+#pragma unroll
+        for (int q = 0; q < (int)(sizeof(Part) / 4); ++q) {
+          float* v = reinterpret_cast<float*>(&on) + q;
+          *v = __shfl_sync(kFull, *v, 0);
+        }
+        side ^= 1;
+        bad = lost;
+      }
+      const bool write = me.rank == 0 && lane == 0;
+      r = finish_row(on, a, w, me.tail, write ? a.loss + me.row : nullptr,
+                     write && a.stats ? a.stats + me.row * 6 : nullptr);
+      if (bad) {
+        r.coef = r.poison = nan;
+        r.dead = w == 0.0f;
+        if (write) {
+          a.loss[me.row] = nan;
+          if (a.stats)
+            for (int q = 0; q < 6; ++q) a.stats[me.row * 6 + q] = nan;
+        }
+      }
+      if (GRAD) {
+        if (lane == 0) row_sh[turn] = r;
+        __syncwarp();
+        bar_sync(kRowDone, kThreads);
+      }
+    }
+    last = me;
+    last_r = r;
+    last_n = bad ? 0 : n;
+    last_end = end;
+    if (more) {
+      me = nx;
+      prepare(me, turn ^ 1);
+    }
+  }
+  if (GRAD) {
+    __syncwarp();
+    bar_sync(kStored, kThreads);
+    finish_grad(last, turn ^ 1, last_r, last_n, last_end);
+  }
+  if (cluster > 1) cg::this_cluster().sync();
+}
+
+// ---------------------------------------------------------------------------
+// Short rows: a warp takes one after another by itself, with its next one's
+// logits and packet on their way to shared memory meanwhile; no warp waits for
+// another.  Otherwise as above: the packet's logits are taken out of the buffer
+// (one entry per lane), which leaves -Inf there, the row is then kept in
+// registers, and the packet's gradients are written over the row's.
+// ---------------------------------------------------------------------------
+
+constexpr int kShortWarps = 4;  // per CTA
+
+// Shared memory of one warp: the row buffer, the row's ends, two packets and
+// the current one's logits on both sides.
+__host__ __device__ constexpr size_t short_smem(int cap, int kpad) {
+  return (size_t)cap * 16 + 64 + (size_t)kpad * 24;
+}
+
+template <typename T, int NV, bool LOSS, bool GRAD>
+__global__ void __launch_bounds__(kShortWarps * 32, 8)
+    distill_short(DistillArgs a, int per, int shares, int64_t items, int kpad) {
+  using S = Slot<T>;
+  constexpr int N = S::N;
+  constexpr int kCap = 32 * NV;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int group = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
+  unsigned char* base = smem + (size_t)group * short_smem(kCap, kpad);
   uint4* buf = reinterpret_cast<uint4*>(base);
   float* ends = reinterpret_cast<float*>(base + (size_t)kCap * 16);
   float* sx = ends + 16;  // student at the packet's positions
   float* tx = sx + kpad;  // teacher
-  auto sync = [] {
-    if (GROUP == 32) __syncwarp();
-    else __syncthreads();
-  };
   pdl_wait();
   const int vocab = a.vocab;
   const float c = a.c;
-  const int cl_rank = LOSS ? (int)(blockIdx.x % cluster) : 0;
-  const int64_t step = (int64_t)(gridDim.x / cluster) * kGroups;
+  const int64_t step = (int64_t)gridDim.x * kShortWarps;
 
   // what is known of the next item before it is worked on
   struct Next {
@@ -500,7 +849,7 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
   } nx;
   auto fetch = [&](int64_t item, int turn) {
     nx.row = LOSS ? item : item / shares;
-    nx.rank = LOSS ? cl_rank : (int)(item - nx.row * shares);
+    nx.rank = LOSS ? 0 : (int)(item - nx.row * shares);
     const T* x = static_cast<const T*>(a.logits) + nx.row * a.stride;
     nx.shape = S::shape(x, vocab);
     nx.lo = (int)min((int64_t)nx.rank * per, (int64_t)nx.shape.slots);
@@ -508,42 +857,45 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
     const uint4* src = reinterpret_cast<const uint4*>(x + nx.shape.head) + nx.lo;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int q = v * GROUP + tid;
+      const int q = v * 32 + lane;
       if (q < nx.held) copy_async16(buf + q, src + q);
     }
     float* packet = tx + (1 + 2 * turn) * kpad;
-    for (int j = tid; j < a.k; j += GROUP) {
+    for (int j = lane; j < a.k; j += 32) {
       copy_async4(packet + j, a.indices + nx.row * a.k + j);
       copy_async4(packet + kpad + j, a.values + nx.row * a.k + j);
     }
     nx.count = a.counts ? a.counts[nx.row] : a.k;
     nx.row_grad = GRAD && a.row_grad ? a.row_grad[nx.row] : 1.0f;
     nx.tail = LOSS && a.tail ? a.tail[nx.row] : 0.0f;
-    if (nx.rank == 0 && tid < nx.shape.edge) nx.end = x[S::edge_at(nx.shape, tid)];
+    if (nx.rank == 0 && lane < nx.shape.edge) nx.end = x[S::edge_at(nx.shape, lane)];
   };
 
-  int64_t item = (int64_t)(blockIdx.x / cluster) * kGroups + group;
+  int64_t item = (int64_t)blockIdx.x * kShortWarps + group;
+  if (LOSS) {
+    // slots past a row's share read as -Inf; `held` varies by one with a row's
+    // place in its blocks, so the last of them is written again for each row
+#pragma unroll
+    for (int v = 0; v < NV; ++v) buf[v * 32 + lane] = S::none();
+  }
   if (item < items) fetch(item, 0);
   int turn = 0;  // the packet buffers in use
-  int side = 0;  // the copy of `whole` in use: the cluster barrier of one row ends
-                 // the reads of the row before it
-  // (the groups of a CTA may differ in their number of items only where they
-  // are warps, which never wait for one another)
   for (; item < items; item += step, turn ^= 1) {
     const Next me = nx;
     T* g = GRAD ? static_cast<T*>(a.grad) + me.row * a.grad_stride : nullptr;
     const int32_t* idx = reinterpret_cast<const int32_t*>(tx + (1 + 2 * turn) * kpad);
     const float* val = tx + (2 + 2 * turn) * kpad;
-    const bool has_edge = me.rank == 0 && tid < me.shape.edge;
+    const bool has_edge = me.rank == 0 && lane < me.shape.edge;
     const int n = min(max(me.count, 0), a.k);
     const float w = GRAD ? me.row_grad * a.inv_tau : 0.0f;
     float end = kNegInf;
-    if (has_edge) ends[tid] = end = to_f32(me.end);
+    if (has_edge) ends[lane] = end = to_f32(me.end);
+    if (LOSS && lane == 31 && me.held < per) buf[me.held] = S::none();
 
     copy_async_wait();
-    sync();
+    __syncwarp();
     bool bad = false;
-    for (int j = tid; j < n; j += GROUP) {
+    for (int j = lane; j < n; j += 32) {
       const int i = idx[j], before = j > 0 ? idx[j - 1] : -1;
       const int pos = i - me.shape.head, q = pos - me.lo * N;
       float s = kNegInf;
@@ -563,38 +915,33 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
       sx[j] = s;
       tx[j] = s == kNegInf ? kNegInf : val[j];
     }
-    if (GROUP == 32) {
-      bad = __any_sync(kFull, bad);
-      __syncwarp();
-    } else {
-      bad = __syncthreads_or(bad) != 0;
-    }
+    bad = __any_sync(kFull, bad);
+    __syncwarp();
     uint4 raw[NV];
-    float m = kNegInf;
-    if (LOSS && has_edge) m = end = ends[tid];
+    SlotMax<T> slot_max;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      raw[v] = buf[v * GROUP + tid];
-      if ((v + 1) * GROUP > me.held && v * GROUP + tid >= me.held) raw[v] = S::none();
-      if (LOSS) m = fmaxf(m, S::max(raw[v]));
+      raw[v] = buf[v * 32 + lane];
+      if (LOSS) slot_max.add(raw[v]);
       forget(raw[v]);
     }
+    if (LOSS && has_edge) end = ends[lane];
     // this thread's slots are in its registers
     if (item + step < items) fetch(item + step, turn ^ 1);
 
     const bool skip = GRAD && !LOSS && w == 0.0f;
     if (bad || skip) {
       const float nan = __int_as_float(0x7FFFFFFF);
-      if (LOSS && me.rank == 0 && tid == 0) {
+      if (LOSS && me.rank == 0 && lane == 0) {
         a.loss[me.row] = nan;
         if (a.stats)
           for (int q = 0; q < 6; ++q) a.stats[me.row * 6 + q] = nan;
       }
       if (GRAD) {
         const T fill = from_f32<T>(w == 0.0f ? 0.0f : nan);
-        if (has_edge) g[S::edge_at(me.shape, tid)] = fill;
+        if (has_edge) g[S::edge_at(me.shape, lane)] = fill;
         T* out = g + me.shape.head + me.lo * N;
-        for (int i = tid; i < me.held * N; i += GROUP) out[i] = fill;
+        for (int i = lane; i < me.held * N; i += 32) out[i] = fill;
       }
       continue;
     }
@@ -602,26 +949,26 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
     Row r;
     if (LOSS) {
       Part p = no_part();
-      p.m_off = warp_max(m);
+      p.m_off = warp_max(fmaxf(slot_max.get(), end));
       const float ref = finite_ref(p.m_off);
-      float s = exp2_fast((end - ref) * c);
+      float2 sum = make_float2(exp2_fast((end - ref) * c), 0.0f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float2 f[N / 2];
         exp2_slot<T>(raw[v], ref, c, 0.0f, f);
-        s += sum_slot<T>(f);
+        sum_slot<T>(f, sum);
         forget(raw[v]);
       }
-      p.s_off = warp_sum(s);
-      if (warp * 32 < n) {
-        for (int j = tid; j < n; j += GROUP) {
+      p.s_off = warp_sum(sum.x + sum.y);
+      if (n > 0) {
+        for (int j = lane; j < n; j += 32) {
           p.m_s = fmaxf(p.m_s, sx[j]);
           p.m_t = fmaxf(p.m_t, tx[j]);
         }
         p.m_s = warp_max(p.m_s);
         p.m_t = warp_max(p.m_t);
         const float rs = finite_ref(p.m_s), rt = finite_ref(p.m_t);
-        for (int j = tid; j < n; j += GROUP) {
+        for (int j = lane; j < n; j += 32) {
           const float y = tx[j] - rt, z = sx[j] - rs;
           const float e = exp2_fast(y * c);
           p.s_s += exp2_fast(z * c);
@@ -632,31 +979,9 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
         p.s_t = warp_sum(p.s_t);
         p.u = warp_sum(p.u);
       }
-      float* loss_out = me.rank == 0 && tid == 0 ? a.loss + me.row : nullptr;
-      float* stats_out = me.rank == 0 && tid == 0 && a.stats ? a.stats + me.row * 6 : nullptr;
-      if (kWarps == 1) {
-        r = finish_row(p, a, w, me.tail, loss_out, stats_out);
-      } else {
-        // one warp joins the warps' parts (sixteen at it took a sixth of all
-        // instructions)
-        if (lane == 0) parts[warp] = p;
-        __syncthreads();
-        if (warp == 0) p = join(lane < kWarps ? parts[lane] : no_part(), kWarps, c);
-        if (cluster > 1) {
-          if (tid == 0) whole[side] = p;
-          cg::this_cluster().sync();
-          if (warp == 0)
-            p = join(lane < cluster ? *cg::this_cluster().map_shared_rank(&whole[side], lane)
-                                    : no_part(),
-                     cluster, c);
-          side ^= 1;
-        }
-        if (tid == 0) row_sh = finish_row(p, a, w, me.tail, loss_out, stats_out);
-        if (GRAD) {
-          __syncthreads();
-          r = row_sh;
-        }
-      }
+      float* loss_out = me.rank == 0 && lane == 0 ? a.loss + me.row : nullptr;
+      float* stats_out = me.rank == 0 && lane == 0 && a.stats ? a.stats + me.row * 6 : nullptr;
+      r = finish_row(p, a, w, me.tail, loss_out, stats_out);
     } else {
       r = stored_row(a, me.row, w);
     }
@@ -666,37 +991,25 @@ __global__ void __launch_bounds__(GROUP < 128 ? 128 : GROUP, 1024 / (GROUP < 128
       uint4* out = reinterpret_cast<uint4*>(g + me.shape.head) + me.lo;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int q = v * GROUP + tid;
+        const int q = v * 32 + lane;
         if (q >= me.held) continue;
         float2 f[N / 2];
         exp2_slot<T>(raw[v], r.ref, c, r.k2, f);
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) f[e] = mul2(f[e], make_float2(coef, coef));
         const uint4 o = r.dead ? make_uint4(0, 0, 0, 0) : S::pack(f);
-        if (SAME) {
-          __stcs(out + q, o);
-        } else {
-          union {
-            uint4 v;
-            T e[N];
-          } u;
-          u.v = o;
-#pragma unroll
-          for (int e = 0; e < N; ++e) reinterpret_cast<T*>(out)[q * N + e] = u.e[e];
-        }
+        __stcs(out + q, o);
       }
       if (has_edge) {
         const float f = coef * exp2_fast(fmaf(end - r.ref, c, -r.k2));
-        g[S::edge_at(me.shape, tid)] = from_f32<T>(r.dead ? 0.0f : f);
+        g[S::edge_at(me.shape, lane)] = from_f32<T>(r.dead ? 0.0f : f);
       }
-      sync();
+      __syncwarp();
       if (!r.dead)
-        for (int j = tid; j < n; j += GROUP)
+        for (int j = lane; j < n; j += 32)
           if (sx[j] != kNegInf) g[idx[j]] = from_f32<T>(grad_on(r, c, sx[j], tx[j]));
     }
   }
-  // the others' reads of this CTA's last part
-  if (LOSS && cluster > 1) cg::this_cluster().sync();
 }
 
 ef_status check_packets(const void* logits, int size, int64_t rows, int64_t vocab, int32_t k,
@@ -720,52 +1033,68 @@ ef_status check_grad(const void* logits, int size, int64_t rows, int64_t vocab, 
   return EF_OK;
 }
 
-constexpr int kMaxCluster = 8;
-
 template <typename T, bool GRAD, bool SAME>
 void launch_chunks(const DistillArgs& a, int64_t rows, int per, cudaStream_t s) {
   launch_cluster_pdl(distill_chunks<T, 512, 8, GRAD, SAME>, kMaxCluster,
                      dim3((unsigned)(rows * kMaxCluster)), dim3(512), 0, s, a, per, kMaxCluster);
 }
 
-template <typename T, int GROUP, int NV, bool LOSS, bool GRAD, bool SAME>
+// CTAs of a persistent kernel: as many as fit the device, at most `most`.
+int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
+  int fit = (int)(225 * 1024 / (smem + 2048));
+  if (fit > by_threads) fit = by_threads;
+  if (fit < 1) fit = 1;
+  return (int64_t)sms * fit < most ? (int64_t)sms * fit : most;
+}
+
+template <typename T, int WARPS, int NV, bool LOSS, bool GRAD, bool SAME>
 void launch_stream(const DistillArgs& a, int64_t rows, int per, int cluster, int shares, int sms,
                    cudaStream_t s) {
-  constexpr int kThreads = GROUP < 128 ? 128 : GROUP, kGroups = kThreads / GROUP;
-  const auto kernel = distill_stream<T, GROUP, NV, LOSS, GRAD, SAME>;
+  const auto kernel = distill_stream<T, WARPS, NV, LOSS, GRAD, SAME>;
   const int kpad = (a.k + 3) & ~3;
-  const size_t smem = kGroups * stream_smem(GROUP * NV, kpad);
-  // CTAs that fit an SM: the registers' bound (launch bounds) and shared memory's
-  int fit = (int)(225 * 1024 / (smem + 2048));
-  if (fit > 1024 / kThreads) fit = 1024 / kThreads;
-  if (fit < 1) fit = 1;
+  const size_t smem = stream_smem((WARPS - 1) * 32 * NV, kpad);
   const int64_t items = LOSS ? rows : rows * shares;
-  int64_t grid = (int64_t)sms * fit / cluster;
-  const int64_t most = (items + kGroups - 1) / kGroups;
-  if (grid > most) grid = most;
+  const int64_t grid = resident(sms, 32 / WARPS, smem, items * cluster) / cluster;
   (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (cluster == 1)
-    launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, s, a, per, 1, shares, items,
+    launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a, per, 1, shares, items,
                kpad);
   else
-    launch_cluster_pdl(kernel, cluster, dim3((unsigned)(grid * cluster)), dim3(kThreads), smem, s,
-                       a, per, cluster, shares, items, kpad);
+    launch_cluster_pdl(kernel, cluster, dim3((unsigned)(grid * cluster)), dim3(WARPS * 32), smem,
+                       s, a, per, cluster, shares, items, kpad);
 }
+
+template <typename T, int NV, bool LOSS, bool GRAD>
+void launch_short(const DistillArgs& a, int64_t rows, int per, int shares, int sms,
+                  cudaStream_t s) {
+  const auto kernel = distill_short<T, NV, LOSS, GRAD>;
+  const int kpad = (a.k + 3) & ~3;
+  const size_t smem = kShortWarps * short_smem(32 * NV, kpad);
+  const int64_t items = LOSS ? rows : rows * shares;
+  const int64_t grid = resident(sms, 8, smem, (items + kShortWarps - 1) / kShortWarps);
+  (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch_pdl(kernel, dim3((unsigned)grid), dim3(kShortWarps * 32), smem, s, a, per, shares, items,
+             kpad);
+}
+
+// Slots that a CTA of W warps holds.
+constexpr int held_by(int warps, int nv) { return (warps - 1) * 32 * nv; }
 
 template <typename T, bool LOSS, bool GRAD>
 void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
   const int64_t slots = a.vocab / Slot<T>::N + 1;
+  constexpr int kMost = held_by(16, 8);
   int cluster = 1, shares = 1;
   if (LOSS) {
     // a row on one CTA while it fits its registers and there are rows enough
     // to fill the device; otherwise on the fewest CTAs for which that holds
     while (cluster < kMaxCluster &&
-           (slots > (int64_t)cluster * 4096 || (rows * cluster < sms && slots > cluster * 256)))
+           (slots > (int64_t)cluster * kMost || (rows * cluster < sms && slots > cluster * 256)))
       cluster *= 2;
   } else {
-    // no sums: a row is cut into shares of at most 2048 slots, shorter ones
-    // while that leaves SMs without work
-    int64_t share = 2048;
+    // no sums: a row is cut into shares of at most one CTA of 8 warps, shorter
+    // ones while that leaves SMs without work
+    int64_t share = held_by(8, 8);
     while (share > 256 && rows * ((slots + share - 1) / share) < 2 * sms) share /= 2;
     shares = (int)((slots + share - 1) / share);
   }
@@ -777,7 +1106,7 @@ void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
                0 &&
            (rows == 1 || (a.grad_stride - a.stride) % Slot<T>::N == 0);
   if constexpr (LOSS) {
-    if (per > 4096) {
+    if (per > kMost) {
       if (same) launch_chunks<T, GRAD, true>(a, rows, per, s);
       else if constexpr (GRAD) launch_chunks<T, GRAD, false>(a, rows, per, s);
       return;
@@ -785,28 +1114,35 @@ void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
   }
   if constexpr (GRAD)
     if (!same) {
-      if (per <= 1024 && cluster == 1)
-        launch_stream<T, 128, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
+      if (per <= held_by(4, 8) && cluster == 1)
+        launch_stream<T, 4, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
       else
-        launch_stream<T, 512, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
+        launch_stream<T, 16, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
       return;
     }
   if (cluster > 1) {
     if constexpr (LOSS) {
-      if (per <= 512) launch_stream<T, 512, 1, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
-      else if (per <= 1024) launch_stream<T, 512, 2, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
-      else launch_stream<T, 512, 8, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
+      if (per <= held_by(16, 1))
+        launch_stream<T, 16, 1, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
+      else if (per <= held_by(16, 4))
+        launch_stream<T, 16, 4, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
+      else
+        launch_stream<T, 16, 8, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
     }
     return;
   }
-  if (per <= 32) launch_stream<T, 32, 1, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 64) launch_stream<T, 32, 2, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 128) launch_stream<T, 32, 4, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 256) launch_stream<T, 32, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 512) launch_stream<T, 128, 4, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 1024) launch_stream<T, 128, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else if (per <= 2048) launch_stream<T, 256, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else launch_stream<T, 512, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  if (per <= 32) launch_short<T, 1, LOSS, GRAD>(a, rows, per, shares, sms, s);
+  else if (per <= 64) launch_short<T, 2, LOSS, GRAD>(a, rows, per, shares, sms, s);
+  else if (per <= 128) launch_short<T, 4, LOSS, GRAD>(a, rows, per, shares, sms, s);
+  else if (per <= 256) launch_short<T, 8, LOSS, GRAD>(a, rows, per, shares, sms, s);
+  else if (per <= held_by(4, 4))
+    launch_stream<T, 4, 4, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  else if (per <= held_by(4, 8))
+    launch_stream<T, 4, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  else if (per <= held_by(8, 8))
+    launch_stream<T, 8, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  else
+    launch_stream<T, 16, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
 }
 
 template <bool LOSS, bool GRAD>

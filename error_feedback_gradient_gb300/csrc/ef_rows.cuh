@@ -100,6 +100,74 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
 }
 
 // ---------------------------------------------------------------------------
+// Asynchronous copies to shared memory, and the barriers between the warps of a
+// CTA that work on different steps of a row.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Named barriers (1..15) over `threads` threads of the CTA.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// Waits for the phase of the given parity, at most kWaitLimitNs; false if it
+// ran out.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+// One copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) that
+// completes on `bar`.
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+// Orders this thread's writes to shared memory before later bulk copies into it.
+__device__ __forceinline__ void fence_bulk() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Rows in 16-byte slots.
 //
 // A row starts anywhere (an odd vocabulary in 16-bit logits), so its vectors
@@ -135,7 +203,7 @@ struct Slot {
   static __device__ __forceinline__ uint4 pack(const float2 (&f)[N / 2]);
   static __device__ __forceinline__ void unpack(const uint4& r, float2 (&f)[N / 2]);
   static __device__ __forceinline__ uint4 none();  // -Inf everywhere
-  static __device__ __forceinline__ float max(const uint4& r);
+  static __device__ __forceinline__ void add(const uint4& r, float d, float2 (&f)[N / 2]);
   // replaces the elements whose bit is set by -Inf
   static __device__ __forceinline__ void mask(uint4& r, uint32_t bits);
 };
@@ -260,27 +328,74 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return bits_pair(r);
 }
 
-// Largest element, NaN ignored (16-bit types: two at a time).
+// The slot's elements plus d, in fp32 (one instruction per element: the 16-bit
+// types are widened by the addition itself).
 template <>
-__device__ __forceinline__ float Slot<float>::max(const uint4& r) {
-  return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
-               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+__device__ __forceinline__ void Slot<float>::add(const uint4& r, float d, float2 (&f)[2]) {
+  const float2 d2 = make_float2(d, d);
+  unpack(r, f);
+  f[0] = add2(f[0], d2);
+  f[1] = add2(f[1], d2);
 }
+template <>
+__device__ __forceinline__ void Slot<__nv_bfloat16>::add(const uint4& r, float d,
+                                                         float2 (&f)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %3; add.rn.f32.bf16 %1, hi, %3;}"
+        : "=f"(f[i].x), "=f"(f[i].y)
+        : "r"(w[i]), "f"(d));
+}
+template <>
+__device__ __forceinline__ void Slot<__half>::add(const uint4& r, float d, float2 (&f)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.f16 %0, lo, %3; add.rn.f32.f16 %1, hi, %3;}"
+        : "=f"(f[i].x), "=f"(f[i].y)
+        : "r"(w[i]), "f"(d));
+}
+
+// Running maximum over slots, NaN ignored (16-bit types: two elements at a
+// time, widened once at the end).
+template <typename T>
+struct SlotMax;
+template <>
+struct SlotMax<float> {
+  float m = kNegInf;
+  __device__ __forceinline__ void add(const uint4& r) {
+    m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(r.x), __uint_as_float(r.y))),
+              fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
+  __device__ __forceinline__ float get() const { return m; }
+};
 template <typename P>
-__device__ __forceinline__ P max_pairs(const uint4& r) {
-  return __hmax2(__hmax2(reinterpret_cast<const P&>(r.x), reinterpret_cast<const P&>(r.y)),
+__device__ __forceinline__ P max_pairs(P m, const uint4& r) {
+  return __hmax2(__hmax2(m, __hmax2(reinterpret_cast<const P&>(r.x),
+                                    reinterpret_cast<const P&>(r.y))),
                  __hmax2(reinterpret_cast<const P&>(r.z), reinterpret_cast<const P&>(r.w)));
 }
 template <>
-__device__ __forceinline__ float Slot<__nv_bfloat16>::max(const uint4& r) {
-  const float2 p = __bfloat1622float2(max_pairs<__nv_bfloat162>(r));
-  return fmaxf(p.x, p.y);
-}
+struct SlotMax<__nv_bfloat16> {
+  __nv_bfloat162 m = __float2bfloat162_rn(kNegInf);
+  __device__ __forceinline__ void add(const uint4& r) { m = max_pairs(m, r); }
+  __device__ __forceinline__ float get() const {
+    const float2 p = __bfloat1622float2(m);
+    return fmaxf(p.x, p.y);
+  }
+};
 template <>
-__device__ __forceinline__ float Slot<__half>::max(const uint4& r) {
-  const float2 p = __half22float2(max_pairs<__half2>(r));
-  return fmaxf(p.x, p.y);
-}
+struct SlotMax<__half> {
+  __half2 m = __float2half2_rn(kNegInf);
+  __device__ __forceinline__ void add(const uint4& r) { m = max_pairs(m, r); }
+  __device__ __forceinline__ float get() const {
+    const float2 p = __half22float2(m);
+    return fmaxf(p.x, p.y);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // host side
