@@ -1,20 +1,46 @@
 // ef_balance_loss, ef_balance_grad, ef_balance_loss_grad: a router's balance
 // loss, its per-expert counts and its gradient.
 //
-// One CTA per segment: it counts the ids, then a warp takes a token at a
-// time, each lane a fixed set of experts.
+// With the counts c_e known, f_e = experts c_e / (k n) is a constant, and the
+// loss needs no per-expert sum over tokens: sum_e f_e mean_t p_te = mean_t d_t
+// with d_t = sum_e f_e p_te, which the gradient p_te (f_e - d_t) needs anyway.
+// So the ids are counted first, then one pass over the logits gives loss and
+// gradient, and what is left to add up is two numbers per token.  Bound by
+// memory: the logits once in, the gradient once out, the ids once in.
+//
+// A token's experts lie in the lanes of a group of G = 1 .. 32 lanes of a warp,
+// each lane NV cells of N neighbouring experts (16 bytes where the rows allow
+// it, else one element); the maximum, and then the sum and d_t together, are
+// exchanged within the group.  The next token's logits are loaded before the
+// current one is worked on.
+//
+// Segments of a few rounds of tokens are finished by one cluster of CTAs each,
+// in one launch.  Longer ones are cut into tiles over the whole
+// device: zero, count (shared-memory histograms, added to the counts with
+// integer atomics), then the pass, whose last CTA adds the tiles' sums in tile
+// order.
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
 #include "ef_rows.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace ef {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSegBatch = 256;  // segments per launch
-constexpr int kPerLane = EF_MAX_EXPERTS / 32;
+constexpr int kSegBatch = 512;  // segments per launch
+constexpr float kLog2e = 1.4426950408889634f;
+// Rounds of eight CTAs' warps up to which one launch with a cluster per segment
+// beats the launches over the device.
+constexpr int64_t kOneLaunch = 12;
 
 struct SegBatch {
-  int64_t off[kSegBatch + 1];
+  int32_t n;                   // segments
+  int32_t off[kSegBatch + 1];  // tokens
 };
 
 struct BalanceArgs {
@@ -35,104 +61,361 @@ struct BalanceArgs {
   int64_t grad_stride;
 };
 
-template <typename T, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a, SegBatch seg, int first) {
-  __shared__ int32_t cnt[EF_MAX_EXPERTS];
-  __shared__ float f[EF_MAX_EXPERTS];
-  __shared__ float part[EF_MAX_EXPERTS];
-  __shared__ float red[32];
-  __shared__ int32_t n_tok;
-  pdl_wait();
-  const int s = first + (int)blockIdx.x, E = a.experts, tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
-  const int64_t t0 = seg.off[blockIdx.x], t1 = seg.off[blockIdx.x + 1];
-  if (tid == 0) n_tok = 0;
-  for (int e = tid; e < E; e += kThreads) cnt[e] = 0;
-  __syncthreads();
-  if (LOSS) {
-    int n = 0;
-    for (int64_t t = t0 + tid; t < t1; t += kThreads) n += !a.mask || a.mask[t] ? 1 : 0;
-    atomicAdd(&n_tok, n);
-    for (int64_t i = t0 * a.k + tid; i < t1 * a.k; i += kThreads) {
-      const int32_t e = a.ids[i];
-      if (e >= 0 && e < E && (!a.mask || a.mask[i / a.k])) atomicAdd(&cnt[e], 1);
+// N neighbouring elements as they lie in memory.
+template <typename T, int N>
+struct Cell {
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw load(const T* p) {
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  static __device__ __forceinline__ Raw none() { return Slot<T>::none(); }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
+    float2 p[N / 2];
+    Slot<T>::unpack(r, p);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      f[2 * i] = p[i].x;
+      f[2 * i + 1] = p[i].y;
     }
-    __syncthreads();
-  } else {
-    for (int e = tid; e < E; e += kThreads) cnt[e] = a.counts_in[(int64_t)s * E + e];
-    if (tid == 0) n_tok = a.tokens_in[s];
-    __syncthreads();
   }
-  const float inv_n = n_tok > 0 ? 1.0f / (float)n_tok : 0.0f;
-  const float scale = (float)E / (float)a.k * inv_n;
-  for (int e = tid; e < E; e += kThreads) {
-    f[e] = (float)cnt[e] * scale;
-    part[e] = 0.0f;
+  static __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
+    float2 q[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) q[i] = make_float2(f[2 * i], f[2 * i + 1]);
+    __stcs(reinterpret_cast<uint4*>(p), Slot<T>::pack(q));
   }
-  __syncthreads();
-  const float w = GRAD ? (a.seg_grad ? a.seg_grad[s] : 1.0f) * inv_n : 0.0f;
-  float acc[kPerLane] = {};
-  float z2 = 0.0f;
-  for (int64_t t = t0 + warp; t < t1; t += kWarps) {
+};
+template <typename T>
+struct Cell<T, 1> {
+  using Raw = T;
+  static __device__ __forceinline__ Raw load(const T* p) { return *p; }
+  static __device__ __forceinline__ Raw none() { return from_f32<T>(kNegInf); }
+  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_f32(r); }
+  static __device__ __forceinline__ void store(T* p, const float (&f)[1]) {
+    *p = from_f32<T>(f[0]);
+  }
+};
+
+// Counts the ids of tokens [t0, t1) into `cnt` (shared, E zeroed words) and
+// returns this thread's unmasked tokens.
+__device__ __forceinline__ int count_tokens(const BalanceArgs& a, int64_t t0, int64_t t1,
+                                            int32_t* cnt) {
+  int n = 0;
+  const int len = (int)(t1 - t0);
+  const uint8_t* mask = a.mask ? a.mask + t0 : nullptr;
+  for (int t = threadIdx.x; t < len; t += blockDim.x) n += !mask || mask[t] ? 1 : 0;
+  const int32_t* ids = a.ids + t0 * a.k;
+  const int64_t total = (int64_t)len * a.k;
+  for (int64_t from = 0; from < total; from += 1 << 30) {  // 32-bit positions within
+    const uint32_t part = (uint32_t)(total - from < 1 << 30 ? total - from : 1 << 30);
+    for (uint32_t i0 = threadIdx.x; i0 < part; i0 += 4 * blockDim.x) {
+      int32_t e[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t i = i0 + u * blockDim.x;
+        e[u] = i < part ? ids[from + i] : -1;
+        if (mask && i < part) {
+          const int64_t at = from == 0 ? (int64_t)(i / (uint32_t)a.k) : (from + i) / a.k;
+          if (!mask[at]) e[u] = -1;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (e[u] >= 0 && e[u] < a.experts) atomicAdd(&cnt[e[u]], 1);
+    }
+  }
+  return n;
+}
+
+// The pass over tokens first, first + step, .. < t1 (`first` per warp: its
+// groups take neighbouring tokens).  Adds d_t and L_t^2 to the lane's sums (lane
+// 0 of each group holds them).
+template <typename T, int N, int NV, bool GRAD>
+__device__ __forceinline__ void pass_tokens(const BalanceArgs& a, int64_t first, int64_t t1,
+                                            int64_t step, int G, const float* f_sh, float w,
+                                            float* d_sum, float* z_sum) {
+  using C = Cell<T, N>;
+  const int lane = (int)(threadIdx.x & 31), sub = lane & (G - 1), group = lane / G;
+  const int cells = a.experts / N;  // (N divides experts)
+  float f[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int cell = sub + j * G;
+      f[j][i] = cell < cells ? f_sh[cell * N + i] : 0.0f;
+    }
+  typename C::Raw raw[NV];
+  uint8_t keep = 1;
+  const auto load = [&](int64_t t) {
     const T* z = static_cast<const T*>(a.logits) + t * a.stride;
-    T* g = GRAD ? static_cast<T*>(a.grad) + t * a.grad_stride : nullptr;
-    if (a.mask && !a.mask[t]) {
-      if (GRAD)
-        for (int e = lane; e < E; e += 32) g[e] = from_f32<T>(0.0f);
-      continue;
+    keep = t < t1 && a.mask ? a.mask[t] : 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int cell = sub + j * G;
+      raw[j] = C::none();
+      if (t < t1 && cell < cells) raw[j] = C::load(z + cell * N);
     }
-    float p[kPerLane];
+  };
+  load(first + group);
+  for (int64_t base = first; base < t1; base += step) {
+    const int64_t t = base + group;
+    float p[NV][N];
     float m = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      p[i] = e < E ? to_f32(z[e]) : kNegInf;
-      m = fmaxf(m, p[i]);
-    }
-    m = finite_ref(warp_max(m));
-    float sum = 0.0f;
+    for (int j = 0; j < NV; ++j) {
+      C::unpack(raw[j], p[j]);
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) sum += p[i] = exp2f((p[i] - m) * 1.4426950408889634f);
-    sum = warp_sum(sum);
-    const bool none = sum == 0.0f;
+      for (int i = 0; i < N; ++i) m = fmaxf(m, p[j][i]);
+    }
+    const bool on = keep != 0;
+    load(t + step);
+    for (int o = G >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    m = finite_ref(m);
+    float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        p[j][i] = exp2_fast((p[j][i] - m) * kLog2e);
+        sum += p[j][i];
+        dot = fmaf(p[j][i], f[j][i], dot);
+      }
+    for (int o = G >> 1; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(kFull, sum, o);
+      dot += __shfl_xor_sync(kFull, dot, o);
+    }
+    // nothing left in the row (sum 0), or padding: p = 0 and no term
+    const bool none = sum == 0.0f || !on;
     const float inv = none ? 0.0f : 1.0f / sum;
-    const float lse = none ? 0.0f : fmaf(log2f(sum), kLn2, m);
-    float dot = 0.0f;
+    const float lse = none ? 0.0f : fmaf(log2_fast(sum), kLn2, m);
+    dot = none ? 0.0f : dot * inv;
+    if (t < t1) {
+      if (sub == 0) {
+        *d_sum += dot;
+        *z_sum = fmaf(lse, lse, *z_sum);
+      }
+      if (GRAD) {
+        // p (alpha (f - d) + 2 beta L) w
+        const float aw = none ? 0.0f : a.alpha * w * inv;
+        const float b = none ? 0.0f : w * inv * (2.0f * a.beta * lse - a.alpha * dot);
+        T* g = static_cast<T*>(a.grad) + t * a.grad_stride;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      p[i] *= inv;
-      acc[i] += p[i];
-      dot += e < E ? p[i] * f[e] : 0.0f;
-    }
-    z2 += lse * lse;
-    if (GRAD) {
-      dot = warp_sum(dot);
-      const float base = 2.0f * a.beta * lse;
+        for (int j = 0; j < NV; ++j) {
+          const int cell = sub + j * G;
+          if (cell >= cells) continue;
+          float d[N];
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E) g[e] = from_f32<T>(w * p[i] * (a.alpha * (f[e] - dot) + base));
+          for (int i = 0; i < N; ++i) d[i] = none ? 0.0f : p[j][i] * fmaf(aw, f[j][i], b);
+          C::store(g + cell * N, d);
+        }
       }
     }
   }
-  if (!LOSS) return;
-  if (s == 0 && tid == 0) a.ws->status = EF_OK;
-  for (int q = 0; q < kWarps; ++q) {  // the warps in order
-    if (warp == q)
-#pragma unroll
-      for (int i = 0; i < kPerLane; ++i)
-        if (lane + 32 * i < E) part[lane + 32 * i] += acc[i];
+}
+
+__device__ __forceinline__ float loss_of(const BalanceArgs& a, float d_sum, float z_sum, int n) {
+  if (n <= 0) return 0.0f;
+  const float inv_n = 1.0f / (float)n;
+  return (a.alpha * d_sum + (a.beta != 0.0f ? a.beta * z_sum : 0.0f)) * inv_n;
+}
+
+// Sums of a block's two values, in every thread; the order is fixed.
+__device__ __forceinline__ float2 block_sum2(float2 v, float* scratch) {
+  v.x = block_sum(v.x, scratch);
+  v.y = block_sum(v.y, scratch);
+  return v;
+}
+
+// One cluster of CTAs per segment: counts, sums and gradients in one launch.
+template <typename T, int N, int NV, bool GRAD>
+__global__ void __launch_bounds__(kThreads) balance_segment(BalanceArgs a, SegBatch seg, int first,
+                                                            int cluster, int G) {
+  __shared__ int32_t cnt[EF_MAX_EXPERTS];
+  __shared__ float f[EF_MAX_EXPERTS];
+  __shared__ float red[32];
+  __shared__ int32_t n_tok;
+  __shared__ float2 sums;
+  const int tid = threadIdx.x, E = a.experts;
+  for (int e = tid; e < E; e += kThreads) cnt[e] = 0;
+  if (tid == 0) n_tok = 0;
+  __syncthreads();
+  pdl_wait();
+  const int local = (int)blockIdx.x / cluster, rank = (int)blockIdx.x % cluster;
+  const int s = first + local;
+  const int64_t off = seg.off[local], len = seg.off[local + 1] - off;
+  const int64_t t0 = off + len * rank / cluster, t1 = off + len * (rank + 1) / cluster;
+  const int mine = count_tokens(a, t0, t1, cnt);
+  if (mine != 0) atomicAdd(&n_tok, mine);
+  int n = 0;
+  const float scale = (float)E / (float)a.k;
+  if (cluster > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int r = 0; r < cluster; ++r) n += *cl.map_shared_rank(&n_tok, r);
+    const float by_n = n > 0 ? scale / (float)n : 0.0f;
+    for (int e = tid; e < E; e += kThreads) {
+      int32_t c = 0;
+      for (int r = 0; r < cluster; ++r) c += *cl.map_shared_rank(&cnt[e], r);
+      f[e] = (float)c * by_n;
+      if (rank == 0) a.counts[(int64_t)s * E + e] = c;
+    }
+  } else {
+    __syncthreads();
+    n = n_tok;
+    const float by_n = n > 0 ? scale / (float)n : 0.0f;
+    for (int e = tid; e < E; e += kThreads) {
+      f[e] = (float)cnt[e] * by_n;
+      a.counts[(int64_t)s * E + e] = cnt[e];
+    }
+  }
+  __syncthreads();
+  const float w = GRAD && n > 0 ? (a.seg_grad ? a.seg_grad[s] : 1.0f) / (float)n : 0.0f;
+  const int per_warp = 32 / G;
+  float2 v = make_float2(0.0f, 0.0f);
+  pass_tokens<T, N, NV, GRAD>(a, t0 + (tid >> 5) * per_warp, t1, kWarps * per_warp, G, f, w, &v.x,
+                              &v.y);
+  v = block_sum2(v, red);
+  if (cluster > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (tid == 0) sums = v;
+    cl.sync();
+    if (rank == 0 && tid == 0) {
+      v = make_float2(0.0f, 0.0f);
+      for (int r = 0; r < cluster; ++r) {
+        const float2 q = *cl.map_shared_rank(&sums, r);
+        v.x += q.x;
+        v.y += q.y;
+      }
+    }
+    cl.sync();
+  }
+  if (rank == 0 && tid == 0) {
+    a.tokens[s] = n;
+    a.loss[s] = loss_of(a, v.x, v.y, n);
+    if (s == 0) a.ws->status = EF_OK;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Long segments, over the whole device.
+// ---------------------------------------------------------------------------
+
+// Workspace behind the header: a ticket, then one pair of sums per (tile,
+// segment) the tile meets; slot tile + segment is different for each such pair
+// because tiles and segments advance together.
+struct TileSums {
+  uint32_t ticket;
+  uint32_t pad[63];
+  float2 sums[1];
+};
+
+__global__ void __launch_bounds__(kThreads) balance_zero(BalanceArgs a, int nseg, TileSums* ts) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i < (int64_t)nseg * a.experts) a.counts[i] = 0;
+  if (i < nseg) a.tokens[i] = 0;
+  if (i == 0) {
+    ts->ticket = 0;
+    a.ws->status = EF_OK;
+  }
+}
+
+// Segment of token t: the last one that starts at or before it and is not
+// empty there.
+__device__ __forceinline__ int segment_at(const SegBatch& seg, int64_t t) {
+  int lo = 0, hi = seg.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seg.off[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) balance_count(BalanceArgs a, SegBatch seg, int64_t t0,
+                                                          int tile) {
+  __shared__ int32_t cnt[EF_MAX_EXPERTS];
+  __shared__ int32_t n_tok;
+  for (int e = threadIdx.x; e < a.experts; e += kThreads) cnt[e] = 0;
+  if (threadIdx.x == 0) n_tok = 0;
+  __syncthreads();
+  pdl_wait();
+  const int64_t from = t0 + (int64_t)blockIdx.x * tile;
+  const int64_t to = min(from + tile, (int64_t)seg.off[seg.n]);
+  for (int s = segment_at(seg, from); s < seg.n && seg.off[s] < to; ++s) {
+    const int64_t b = max(from, (int64_t)seg.off[s]), e1 = min(to, (int64_t)seg.off[s + 1]);
+    if (b >= e1) continue;
+    const int mine = count_tokens(a, b, e1, cnt);
+    if (mine != 0) atomicAdd(&n_tok, mine);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+      if (cnt[e] != 0) atomicAdd(&a.counts[(int64_t)s * a.experts + e], cnt[e]);
+      cnt[e] = 0;
+    }
+    if (threadIdx.x == 0) {
+      if (n_tok != 0) atomicAdd(&a.tokens[s], n_tok);
+      n_tok = 0;
+    }
     __syncthreads();
   }
-  float b = 0.0f;
-  for (int e = tid; e < E; e += kThreads) b += f[e] * part[e];
-  b = block_sum(b, red);
-  z2 = block_sum(lane == 0 ? z2 : 0.0f, red);
-  for (int e = tid; e < E; e += kThreads) a.counts[(int64_t)s * E + e] = cnt[e];
+}
+
+// `a.counts_in`, `a.tokens_in`, `a.seg_grad`, `a.loss` start at the batch.
+template <typename T, int N, int NV, bool LOSS, bool GRAD>
+__global__ void __launch_bounds__(kThreads) balance_tiles(BalanceArgs a, SegBatch seg, int64_t t0,
+                                                          int tile, int G, TileSums* ts) {
+  __shared__ float f[EF_MAX_EXPERTS];
+  __shared__ float red[32];
+  __shared__ bool is_last;
+  pdl_wait();
+  const int tid = threadIdx.x, E = a.experts;
+  const int64_t from = t0 + (int64_t)blockIdx.x * tile;
+  const int64_t to = min(from + tile, (int64_t)seg.off[seg.n]);
+  const int per_warp = 32 / G;
+  const float scale = (float)E / (float)a.k;
+  for (int s = segment_at(seg, from); s < seg.n && seg.off[s] < to; ++s) {
+    const int64_t b = max(from, (int64_t)seg.off[s]), e1 = min(to, (int64_t)seg.off[s + 1]);
+    if (b >= e1) continue;
+    const int n = a.tokens_in[s];
+    const float by_n = n > 0 ? scale / (float)n : 0.0f;
+    __syncthreads();
+    for (int e = tid; e < E; e += kThreads)
+      f[e] = (float)a.counts_in[(int64_t)s * E + e] * by_n;
+    __syncthreads();
+    const float w = GRAD && n > 0 ? (a.seg_grad ? a.seg_grad[s] : 1.0f) / (float)n : 0.0f;
+    float2 v = make_float2(0.0f, 0.0f);
+    pass_tokens<T, N, NV, GRAD>(a, b + (tid >> 5) * per_warp, e1, kWarps * per_warp, G, f, w,
+                                &v.x, &v.y);
+    if (LOSS) {
+      v = block_sum2(v, red);
+      if (tid == 0) ts->sums[blockIdx.x + s] = v;
+    }
+  }
+  if (!LOSS) return;
+  // the CTA that finishes last adds up every segment's tiles
   if (tid == 0) {
-    a.tokens[s] = n_tok;
-    a.loss[s] = n_tok > 0 ? (a.alpha * b + (a.beta != 0.0f ? a.beta * z2 : 0.0f)) * inv_n : 0.0f;
+    __threadfence();
+    is_last = atomicAdd(&ts->ticket, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!is_last) return;
+  const int lane = tid & 31;
+  for (int s = tid >> 5; s < seg.n; s += kWarps) {  // a warp per segment
+    float2 v = make_float2(0.0f, 0.0f);
+    if (seg.off[s] < seg.off[s + 1]) {
+      const int64_t lo = (seg.off[s] - t0) / tile, hi = (seg.off[s + 1] - 1 - t0) / tile;
+      for (int64_t i = lo + lane; i <= hi; i += 32) {
+        const float2 q = __ldcg(&ts->sums[i + s]);
+        v.x += q.x;
+        v.y += q.y;
+      }
+    }
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (lane == 0) a.loss[s] = loss_of(a, v.x, v.y, a.tokens_in[s]);
   }
 }
 
@@ -176,7 +459,115 @@ ef_status check_buffers(const BalanceArgs& a, int size, int64_t tokens, int32_t 
   return any_overlap(spans, 11) ? EF_ERR_ALIAS : EF_OK;
 }
 
-size_t workspace_bytes_for() { return sizeof(WsHeader); }
+// CTAs of the tiled pass: enough to fill any device this library runs on.
+constexpr int kMaxTiles = 2048;
+
+size_t workspace_bytes_for(int32_t nseg) {
+  const int batch = nseg < kSegBatch ? nseg : kSegBatch;
+  return sizeof(WsHeader) + sizeof(TileSums) + (size_t)(kMaxTiles + batch) * sizeof(float2);
+}
+
+// The form of the pass: lanes per token and cells per lane.
+struct Form {
+  int G, nv;
+  bool wide;
+};
+Form form_of(const BalanceArgs& a, int size, bool grad) {
+  Form r;
+  const int n = 16 / size;
+  r.wide = a.experts % n == 0 && aligned16(a.logits) && a.stride % n == 0 &&
+           (!grad || (aligned16(a.grad) && a.grad_stride % n == 0));
+  const int cells = r.wide ? a.experts / n : a.experts;
+  // up to 16 elements per lane (8 single ones): few lanes to exchange with, and
+  // several tokens per warp, before the registers of a lane run out
+  const int most = r.wide ? 16 / n : 8;
+  r.G = 1;
+  while (r.G < 32 && r.G * most < cells) r.G *= 2;
+  const int need = (cells + r.G - 1) / r.G;
+  r.nv = 1;
+  while (r.nv < need) r.nv *= 2;
+  return r;
+}
+
+// `F` is called with the cell's elements and the cells per lane as constants.
+template <typename T, typename F>
+void with_form(const Form& form, F f) {
+  constexpr int N = Slot<T>::N;
+  using std::integral_constant;
+  if (form.wide) {
+    if (form.nv == 1) f(integral_constant<int, N>(), integral_constant<int, 1>());
+    else if (form.nv == 2) f(integral_constant<int, N>(), integral_constant<int, 2>());
+    else if (N == 8 || form.nv == 4) f(integral_constant<int, N>(), integral_constant<int, 4>());
+    else f(integral_constant<int, N>(), integral_constant<int, N == 8 ? 4 : 8>());
+  } else {
+    if (form.nv <= 4) f(integral_constant<int, 1>(), integral_constant<int, 4>());
+    else if (form.nv <= 8) f(integral_constant<int, 1>(), integral_constant<int, 8>());
+    else f(integral_constant<int, 1>(), integral_constant<int, 32>());
+  }
+}
+
+template <typename T, bool LOSS, bool GRAD>
+ef_status launch_batch(BalanceArgs a, const SegBatch& seg, int first, int sms, cudaStream_t s) {
+  const Form form = form_of(a, (int)sizeof(T), GRAD);
+  const int64_t t0 = seg.off[0], tokens = seg.off[seg.n] - t0;
+  int64_t longest = 0;
+  for (int i = 0; i < seg.n; ++i)
+    longest = seg.off[i + 1] - seg.off[i] > longest ? seg.off[i + 1] - seg.off[i] : longest;
+  if constexpr (LOSS) {
+    // rounds of a CTA's warps over the longest segment, on a cluster of eight
+    const int64_t round = kWarps * (32 / form.G);
+    if (longest <= kOneLaunch * 8 * round) {
+      // CTAs per segment: one round each, while that leaves SMs idle
+      int cluster = 1;
+      while (cluster < 8 && longest > cluster * round && seg.n * cluster < 4 * sms) cluster *= 2;
+      with_form<T>(form, [&](auto n, auto nv) {
+        const auto kernel = balance_segment<T, n.value, nv.value, GRAD>;
+        if (cluster == 1)
+          launch_pdl(kernel, dim3((unsigned)seg.n), dim3(kThreads), 0, s, a, seg, first, 1,
+                     form.G);
+        else
+          launch_cluster_pdl(kernel, cluster, dim3((unsigned)(seg.n * cluster)), dim3(kThreads),
+                             0, s, a, seg, first, cluster, form.G);
+      });
+      return check_launch();
+    }
+  }
+  TileSums* ts = LOSS ? reinterpret_cast<TileSums*>(a.ws + 1) : nullptr;
+  if (tokens == 0) return EF_OK;  // (a gradient alone: nothing to write)
+  // four CTAs per SM, their tiles whole rounds of the CTA's warps where there
+  // are several of them
+  const int round = kWarps * (32 / form.G);
+  int64_t tile = (tokens + 4 * sms - 1) / (4 * sms);
+  if (tile > 2 * round) tile = (tile + round - 1) / round * round;
+  const int64_t least = (tokens + kMaxTiles - 1) / kMaxTiles;
+  if (tile < least) tile = least;
+  const unsigned tiles = (unsigned)((tokens + tile - 1) / tile);
+  const size_t skip = (size_t)first * a.experts;
+  if constexpr (LOSS) {
+    a.counts += skip;
+    a.tokens += first;
+    a.loss += first;
+    a.counts_in = a.counts;
+    a.tokens_in = a.tokens;
+    const int64_t cells = (int64_t)seg.n * a.experts;
+    launch_pdl(balance_zero, dim3((unsigned)((cells + kThreads - 1) / kThreads)), dim3(kThreads),
+               0, s, a, (int)seg.n, ts);
+    ef_status st = check_launch();
+    if (st != EF_OK) return st;
+    launch_pdl(balance_count, dim3(tiles), dim3(kThreads), 0, s, a, seg, t0, (int)tile);
+    st = check_launch();
+    if (st != EF_OK) return st;
+  } else {
+    a.counts_in += skip;
+    a.tokens_in += first;
+  }
+  if (a.seg_grad) a.seg_grad += first;
+  with_form<T>(form, [&](auto n, auto nv) {
+    launch_pdl(balance_tiles<T, n.value, nv.value, LOSS, GRAD>, dim3(tiles), dim3(kThreads), 0, s,
+               a, seg, t0, (int)tile, form.G, ts);
+  });
+  return check_launch();
+}
 
 template <bool LOSS, bool GRAD>
 ef_status launch(int32_t dtype, const BalanceArgs& a, int32_t nseg, const int64_t* off,
@@ -185,14 +576,13 @@ ef_status launch(int32_t dtype, const BalanceArgs& a, int32_t nseg, const int64_
   ef_status st = current_device(&dev);
   if (st != EF_OK) return st;
   for (int32_t first = 0; first < nseg; first += kSegBatch) {
-    const int n = nseg - first < kSegBatch ? nseg - first : kSegBatch;
     SegBatch b;
-    for (int i = 0; i <= n; ++i) b.off[i] = off[first + i];
+    b.n = nseg - first < kSegBatch ? nseg - first : kSegBatch;
+    for (int i = 0; i <= b.n; ++i) b.off[i] = (int32_t)off[first + i];
     with_dtype(dtype, [&](auto t) {
-      launch_pdl(balance_kernel<decltype(t), LOSS, GRAD>, dim3((unsigned)n), dim3(kThreads), 0,
-                 static_cast<cudaStream_t>(stream), a, b, (int)first);
+      st = launch_batch<decltype(t), LOSS, GRAD>(a, b, first, dev.sms,
+                                                 static_cast<cudaStream_t>(stream));
     });
-    st = check_launch();
     if (st != EF_OK) return st;
   }
   return EF_OK;
@@ -209,7 +599,7 @@ ef_status ef_balance_workspace_size(int64_t tokens, int32_t experts, int32_t k, 
   const ef_status st = ef::check_common(EF_DTYPE_F32, tokens, experts, experts, k, nseg,
                                         h_seg_offsets, 0.0f, 0.0f);
   if (st != EF_OK) return st;
-  *bytes = ef::workspace_bytes_for();
+  *bytes = ef::workspace_bytes_for(nseg);
   return EF_OK;
 }
 
@@ -228,7 +618,7 @@ ef_status ef_balance_loss(const void* logits, int32_t dtype, int64_t tokens, int
   a.loss = out_loss, a.counts = out_counts, a.tokens = out_tokens;
   a.ws = static_cast<WsHeader*>(workspace);
   st = check_buffers(a, dtype_size(dtype), tokens, nseg, true, false, workspace, workspace_bytes,
-                     workspace_bytes_for());
+                     workspace_bytes_for(nseg));
   if (st != EF_OK) return st;
   return launch<true, false>(dtype, a, nseg, h_seg_offsets, stream);
 }
@@ -270,7 +660,7 @@ ef_status ef_balance_loss_grad(const void* logits, int32_t dtype, int64_t tokens
   a.ws = static_cast<WsHeader*>(workspace);
   a.grad = grad, a.grad_stride = grad_stride;
   st = check_buffers(a, dtype_size(dtype), tokens, nseg, true, true, workspace, workspace_bytes,
-                     workspace_bytes_for());
+                     workspace_bytes_for(nseg));
   if (st != EF_OK) return st;
   return launch<true, true>(dtype, a, nseg, h_seg_offsets, stream);
 }

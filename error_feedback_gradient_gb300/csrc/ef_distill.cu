@@ -1054,8 +1054,27 @@ void launch_stream(const DistillArgs& a, int64_t rows, int per, int cluster, int
   const int kpad = (a.k + 3) & ~3;
   const size_t smem = stream_smem((WARPS - 1) * 32 * NV, kpad);
   const int64_t items = LOSS ? rows : rows * shares;
-  const int64_t grid = resident(sms, 32 / WARPS, smem, items * cluster) / cluster;
+  int64_t grid = resident(sms, 32 / WARPS, smem, items * cluster) / cluster;
   (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (cluster > 1 && grid < items) {
+    // clusters stay within parts of the device whose SMs they need not fill:
+    // fewer fit than CTAs would (32 instead of 38 of 8 CTAs, and the other 6
+    // would run alone after them)
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(grid * cluster));
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) == cudaSuccess && fit > 0 &&
+        fit < grid)
+      grid = fit;
+  }
   if (cluster == 1)
     launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a, per, 1, shares, items,
                kpad);
@@ -1083,7 +1102,7 @@ constexpr int held_by(int warps, int nv) { return (warps - 1) * 32 * nv; }
 template <typename T, bool LOSS, bool GRAD>
 void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
   const int64_t slots = a.vocab / Slot<T>::N + 1;
-  constexpr int kMost = held_by(16, 8);
+  constexpr int kMost = held_by(16, 9);
   int cluster = 1, shares = 1;
   if (LOSS) {
     // a row on one CTA while it fits its registers and there are rows enough
@@ -1117,7 +1136,7 @@ void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
       if (per <= held_by(4, 8) && cluster == 1)
         launch_stream<T, 4, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
       else
-        launch_stream<T, 16, 8, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
+        launch_stream<T, 16, 9, LOSS, GRAD, false>(a, rows, per, cluster, shares, sms, s);
       return;
     }
   if (cluster > 1) {
@@ -1127,7 +1146,7 @@ void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
       else if (per <= held_by(16, 4))
         launch_stream<T, 16, 4, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
       else
-        launch_stream<T, 16, 8, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
+        launch_stream<T, 16, 9, LOSS, GRAD, true>(a, rows, per, cluster, 1, sms, s);
     }
     return;
   }
@@ -1141,8 +1160,12 @@ void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
     launch_stream<T, 4, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
   else if (per <= held_by(8, 8))
     launch_stream<T, 8, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
-  else
-    launch_stream<T, 16, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  else if constexpr (LOSS) {
+    if (per <= held_by(16, 8))
+      launch_stream<T, 16, 8, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+    else
+      launch_stream<T, 16, 9, LOSS, GRAD, true>(a, rows, per, 1, shares, sms, s);
+  }
 }
 
 template <bool LOSS, bool GRAD>

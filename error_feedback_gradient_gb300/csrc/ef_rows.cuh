@@ -136,19 +136,25 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 // Waits for the phase of the given parity, at most kWaitLimitNs; false if it
-// ran out.
+// ran out.  (The wait itself suspends the thread for a while; the clock is
+// read only when it comes back empty-handed.)
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
