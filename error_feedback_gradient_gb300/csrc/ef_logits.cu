@@ -53,6 +53,15 @@ struct NanMax<__half> : NanMax16<__half2, __half> {
   static __device__ __forceinline__ P none() { return __float2half2_rn(kNegInf); }
 };
 
+template <typename T>
+struct Lowest {
+  static __device__ __forceinline__ float value() { return -3.402823466e38f; }
+};
+template <>
+struct Lowest<__half> {
+  static __device__ __forceinline__ float value() { return -65504.0f; }
+};
+
 // The value of a key (a NaN key gives a NaN).
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
@@ -149,33 +158,36 @@ __device__ __noinline__ void plain_row(const TopkArgs& a, int64_t row, uint32_t*
 // and an upper key.
 // ---------------------------------------------------------------------------
 
-// A key t with at least k of keys[0..n) at or above it, and not many more:
-// the search stops at k + k / 8 + 4.  Returns 0 if there are fewer than k keys
-// above -Inf.
-__device__ __forceinline__ uint32_t warp_bound(const uint32_t* keys, int n, int k) {
-  const int lane = (int)lane_id();
-  uint32_t hi = 0, lo = 0xFFFFFFFFu;
+// A key t with at least k of a warp's keys at or above it, and not many more:
+// the search stops at `most`.  Returns 0 if fewer than k keys are above -Inf.
+// `each(f)` calls f with every key of this lane.
+template <typename Each>
+__device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
+  uint32_t hi = 0, lo = 0xFFFFFFFFu, any = 0, all = 0xFFFFFFFFu;
   int live = 0;
-  for (int i = lane; i < n; i += 32) {
-    const uint32_t q = keys[i];
+  each([&](uint32_t q) {
     hi = max(hi, q);
     lo = min(lo, q);
+    any |= q;
+    all &= q;
     live += q > kKeyNegInf ? 1 : 0;
-  }
+  });
   hi = __reduce_max_sync(kFull, hi);
+  // bits below `end` are the same in every key (a narrow type's)
+  const uint32_t vary = __reduce_or_sync(kFull, any) & ~__reduce_and_sync(kFull, all);
+  const int end = __ffs(vary) - 1;
   lo = max(__reduce_min_sync(kFull, lo), kKeyNegInf + 1);
   if (__reduce_add_sync(kFull, live) < k) return 0;
   // t keeps count(t) >= k
   uint32_t t = lo;
-  const int most = k + k / 8 + 4;
   const uint32_t differ = hi ^ lo;
   if (differ != 0) {
     const int top = 31 - __clz(differ);
     t = lo & ~((2u << top) - 1u);  // the common prefix: every key is at or above it
-    for (int b = top; b >= 0; --b) {
+    for (int b = top; b >= end; --b) {
       const uint32_t mid = t | (1u << b);
       int c = 0;
-      for (int i = lane; i < n; i += 32) c += keys[i] >= mid ? 1 : 0;
+      each([&](uint32_t q) { c += q >= mid ? 1 : 0; });
       c = __reduce_add_sync(kFull, c);
       if (c >= k) {
         t = mid;
@@ -186,12 +198,329 @@ __device__ __forceinline__ uint32_t warp_bound(const uint32_t* keys, int n, int 
   }
   // the smallest key that is at or above it: a value of the row
   uint32_t snap = 0xFFFFFFFFu;
-  for (int i = lane; i < n; i += 32)
-    if (keys[i] >= t) snap = min(snap, keys[i]);
+  each([&](uint32_t q) {
+    if (q >= t) snap = min(snap, q);
+  });
   return __reduce_min_sync(kFull, snap);
 }
 
+// The bound over keys in shared memory, REGS of them per lane in registers; 0:
+// n of them (a multiple of 4), read four at a time for each step.
+template <int REGS>
+__device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int k) {
+  const int lane = (int)lane_id();
+  const int most = k + k / 4 + 8;
+  if constexpr (REGS > 0) {
+    uint32_t own[REGS];
+#pragma unroll
+    for (int q = 0; q < REGS; ++q) own[q] = keys[q * 32 + lane];
+    return warp_bound(
+        [&](auto f) {
+#pragma unroll
+          for (int q = 0; q < REGS; ++q) f(own[q]);
+        },
+        k, most);
+  } else {
+    const uint4* four = reinterpret_cast<const uint4*>(keys);
+    return warp_bound(
+        [&](auto f) {
+          for (int i = lane; i < n / 4; i += 32) {
+            const uint4 q = four[i];
+            f(q.x);
+            f(q.y);
+            f(q.z);
+            f(q.w);
+          }
+        },
+        k, most);
+  }
+}
+
+// The value a bound stands for; -Inf itself is never a candidate.
+template <typename T>
+__device__ __forceinline__ float bound_value(uint32_t key, int k) {
+  return k == 0 ? __int_as_float(0x7F800000) : key == 0 ? Lowest<T>::value() : key_value(key);
+}
+
 constexpr int kBuckets = 512;
+
+// Elements that are not below t (a NaN is not), for a t that the type holds.
+// take() replaces them by -Inf and returns a word that is not 0 if there were
+// any; it has no branch, which costs less than skipping the slots without any.
+template <typename T>
+struct Above;
+template <>
+struct Above<float> {
+  float t;
+  __device__ __forceinline__ explicit Above(float x) : t(x) {}
+  __device__ __forceinline__ uint32_t take(uint4& r) const {
+    uint32_t some = 0;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(__uint_as_float(w[i]) < t)) {
+        w[i] = 0xFF800000u;
+        some = 1;
+      }
+    return some;
+  }
+};
+template <>
+struct Above<__nv_bfloat16> {
+  __nv_bfloat162 t;
+  __device__ __forceinline__ explicit Above(float x) : t(__float2bfloat162_rn(x)) {}
+  __device__ __forceinline__ uint32_t take(uint4& r) const {
+    uint32_t some = 0;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = __hgeu2_mask(reinterpret_cast<const __nv_bfloat162&>(w[i]), t);
+      w[i] = (w[i] & ~m) | (0xFF80FF80u & m);
+      some |= m;
+    }
+    return some;
+  }
+};
+template <>
+struct Above<__half> {
+  __half2 t;
+  __device__ __forceinline__ explicit Above(float x) : t(__float2half2_rn(x)) {}
+  __device__ __forceinline__ uint32_t take(uint4& r) const {
+    uint32_t some = 0;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = __hgeu2_mask(reinterpret_cast<const __half2&>(w[i]), t);
+      w[i] = (w[i] & ~m) | (0xFC00FC00u & m);
+      some |= m;
+    }
+    return some;
+  }
+};
+
+// Slots that hold candidates: their elements, the first one's position and the
+// bound they were held against.
+struct Hit {
+  uint4 raw;
+  int32_t at;
+  float bound;
+  uint32_t pad[2];
+};
+
+// A whole warp appends the slots of its lanes with `some` set.
+__device__ __forceinline__ void push_hit(bool some, const uint4& raw, int at, float t, int* count,
+                                         Hit* hits, int cap) {
+  const unsigned who = __ballot_sync(kFull, some);
+  if (who == 0) return;
+  int base = 0;
+  if (lane_id() == 0) base = atomicAdd(count, __popc(who));
+  base = __shfl_sync(kFull, base, 0) + __popc(who & lanemask_lt());
+  if (some && base < cap) {
+    hits[base].raw = raw;
+    hits[base].at = at;
+    hits[base].bound = t;
+  }
+}
+
+// The candidates of n slots as keys and positions, in any order; returns their
+// number (more than cap: the rest is not there).
+template <typename T>
+__device__ __forceinline__ int warp_candidates(const Hit* hits, int n, uint32_t* key,
+                                               int32_t* idx, int cap) {
+  constexpr int N = Slot<T>::N;
+  int total = 0;
+  for (int h0 = 0; h0 < n; h0 += 32) {
+    const int h = h0 + (int)lane_id();
+    const T* e = reinterpret_cast<const T*>(&hits[h].raw);
+    uint32_t left = 0;
+    int at = 0;
+    if (h < n) {
+      const uint4 raw = hits[h].raw;
+      const float t = hits[h].bound;
+      at = hits[h].at;
+      float2 f[N / 2];
+      Slot<T>::unpack(raw, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        left |= !((i & 1 ? f[i / 2].y : f[i / 2].x) < t) ? 1u << i : 0u;
+    }
+    for (unsigned who = __ballot_sync(kFull, left != 0); who != 0;
+         who = __ballot_sync(kFull, left != 0)) {
+      if (left != 0) {
+        const int i = __ffs(left) - 1, to = total + __popc(who & lanemask_lt());
+        if (to < cap) {
+          key[to] = order_key(to_f32(e[i]));
+          idx[to] = at + i;
+        }
+        left &= left - 1;
+      }
+      total += __popc(who);
+    }
+  }
+  __syncwarp();
+  return total;
+}
+
+// The packet of at most 32 * PER candidates, which are held in registers.  The
+// k-th largest key is found bit by bit; the packet's places follow from counting
+// positions into buckets, each bucket's few ordered by comparison.  The
+// candidates that are left out are added to the tail as integers, so that
+// their order in the list does not matter: 2^-23 of the largest term each.
+template <int PER>
+__device__ __forceinline__ void warp_emit_few(const TopkArgs& a, int64_t row, int n,
+                                              const uint32_t* key, const int32_t* idx,
+                                              uint32_t* bucket, int32_t* places, float m,
+                                              float s) {
+  constexpr int kB = 256, kPer = kB / 32;  // buckets
+  const int lane = (int)lane_id(), k = a.k;
+  uint32_t kv[PER];
+  int32_t iv[PER];
+  uint4* zero = reinterpret_cast<uint4*>(bucket);
+#pragma unroll
+  for (int q = 0; q < kPer / 4; ++q) zero[q * 32 + lane] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int i = q * 32 + lane;
+    kv[q] = i < n ? key[i] : 0u;  // below every candidate's
+    iv[q] = i < n ? idx[i] : 0;
+  }
+  __syncwarp();
+  const int want = min(k, n);
+  uint32_t cut = kKeyNegInf + 1;  // every candidate
+  unsigned take = 0;              // bit q: this lane's q-th is in the packet
+  bool tied = false;
+  if (n > k) {
+    uint32_t hi = 0, lo = 0xFFFFFFFFu, any = 0, all = 0xFFFFFFFFu;
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (q * 32 + lane < n) {
+        hi = max(hi, kv[q]);
+        lo = min(lo, kv[q]);
+        any |= kv[q];
+        all &= kv[q];
+      }
+    hi = __reduce_max_sync(kFull, hi);
+    lo = __reduce_min_sync(kFull, lo);
+    cut = lo;
+    int at = n;  // keys at or above cut
+    if (hi != lo) {
+      const int top = 31 - __clz(hi ^ lo);
+      // bits below `end` are the same in every key (a narrow type's)
+      const int end =
+          __ffs(__reduce_or_sync(kFull, any) & ~__reduce_and_sync(kFull, all)) - 1;
+      cut = lo & ~((2u << top) - 1u);
+      for (int b = top; b >= end && at != k; --b) {
+        const uint32_t mid = cut | (1u << b);
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) c += kv[q] >= mid ? 1 : 0;
+        c = __reduce_add_sync(kFull, c);
+        if (c >= k) {
+          cut = mid;
+          at = c;
+        }
+      }
+      cut = max(cut | (lo & ((1u << end) - 1u)), lo);
+    }
+    if (at != k) {
+      tied = true;
+      // ties at the cut: the lower positions first
+      int above = 0;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) above += kv[q] > cut ? 1 : 0;
+      const int need = k - __reduce_add_sync(kFull, above);
+      int32_t last = 0x7FFFFFFF;
+      if (at - k <= 16) {
+        // the few that are too many, highest position first
+        for (int drop = at - k; drop > 0; --drop) {
+          int32_t most = -1;
+#pragma unroll
+          for (int q = 0; q < PER; ++q)
+            if (kv[q] == cut && iv[q] < last) most = max(most, iv[q]);
+          last = __reduce_max_sync(kFull, most);
+        }
+      } else {
+        int32_t low = -1;  // positions up to it hold fewer than `need` ties
+        for (int b = 30; b >= 0; --b) {
+          const int32_t mid = low + (1 << b);
+          int c = 0;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) c += kv[q] == cut && iv[q] <= mid ? 1 : 0;
+          if (__reduce_add_sync(kFull, c) < need) low = mid;
+        }
+        last = low + 2;
+      }
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (kv[q] > cut || (kv[q] == cut && iv[q] < last)) take |= 1u << q;
+    }
+  }
+  if (!tied) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (kv[q] >= cut) take |= 1u << q;
+  }
+  if (k == 0) take = 0;  // (candidates are then +Inf and NaN alone)
+  const int bits = 32 - __clz(max(a.vocab - 1, 1));
+  const int shift = max(bits - 8, 0);
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    if (take >> q & 1u) atomicAdd(&bucket[iv[q] >> shift], 1u);
+  __syncwarp();
+  uint32_t cnt[kPer], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    cnt[q] = bucket[lane * kPer + q];
+    sum += cnt[q];
+  }
+  uint32_t base = warp_incl_scan(sum) - sum;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    bucket[lane * kPer + q] = base;  // the bucket's first place; then its next one
+    base += cnt[q];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    if (take >> q & 1u) places[atomicAdd(&bucket[iv[q] >> shift], 1u)] = iv[q];
+  __syncwarp();
+  // bucket b now holds its end, its start is bucket b - 1's end
+  float m2 = kNegInf;
+  bool nan = false;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    if (take >> q & 1u) {
+      const int b = iv[q] >> shift;
+      const uint32_t from = b > 0 ? bucket[b - 1] : 0u, end = bucket[b];
+      uint32_t to = from;
+      for (uint32_t j = from; j < end && end - from > 1; ++j) to += places[j] < iv[q] ? 1u : 0u;
+      a.values[row * k + to] = key_value(kv[q]);
+      a.indices[row * k + to] = iv[q];
+    } else if (q * 32 + lane < n) {
+      const float x = key_value(kv[q]);
+      nan |= !(x <= 3.402823466e38f);  // +Inf too: its sum has no finite logarithm
+      m2 = fmaxf(m2, x);
+    }
+  }
+  for (int j = want + lane; j < k; j += 32) {
+    a.values[row * k + j] = 0.0f;
+    a.indices[row * k + j] = -1;
+  }
+  if (lane == 0) a.counts[row] = want;
+  if (a.tail == nullptr) return;
+  m2 = fmaxf(warp_max(m2), m);
+  const float ref = finite_ref(m2);
+  uint32_t left = 0;
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    if (!(take >> q & 1u) && q * 32 + lane < n)
+      left += __float2uint_rn(exp2_fast((key_value(kv[q]) - ref) * a.c) * 0x1p22f);
+  left = __reduce_add_sync(kFull, left);  // at most 512 terms of 2^22
+  float s2 = (float)left * 0x1p-22f;
+  s2 += m != kNegInf ? s * exp2_fast((m - ref) * a.c) : s;  // (s is 0, or NaN)
+  if (__any_sync(kFull, nan)) s2 = __int_as_float(0x7FFFFFFF);
+  if (lane == 0) a.tail[row] = s2 == 0.0f ? kNegInf : fmaf(ref, a.inv_tau, log2_fast(s2) * kLn2);
+}
 
 // The candidates' packet.  `key`, `idx`: n candidates in any order; `okey`,
 // `oidx`: room for as many; `bucket`: kBuckets words.  Writes the row's packet
@@ -335,30 +664,32 @@ __device__ __forceinline__ void warp_emit(const TopkArgs& a, int64_t row, int n,
 // shared memory ahead of time and finds the bound from the workers' maxima, the
 // second makes the packet of one row while the others read the next.  A row of
 // several chunks keeps its maxima, so the bound rises from chunk to chunk.
-// FINE: a group is a slot position (a few per thread) instead of a thread.
+// GPT: groups per thread (its slots are dealt to them in runs).
 // ---------------------------------------------------------------------------
 
 // (kSummed: two, by turns, so that a row's arrivals never meet the last row's)
 enum TopkBarrier { kReady = 1, kMaxima, kBound, kSummed, kListFree = kSummed + 2 };
 
-template <int WARPS, int NV, bool FINE>
+template <int WARPS, int NV, int GPT>
 struct TopkShape {
   static constexpr int kWorkers = WARPS - 2, kLanes = kWorkers * 32, kCap = kLanes * NV;
-  static constexpr int kGroups = FINE ? kCap : kLanes;
+  static constexpr int kGroups = kLanes * GPT;
+  static_assert(NV % GPT == 0, "groups of equal size");
 };
 
-// Shared memory in bytes: the chunk, the groups' keys, two lists of `cap`
-// candidates (keys, positions) and the order's scratch.
+// Shared memory in bytes: the chunk, the groups' keys, `cap` slots with
+// candidates, and `cap` candidates twice (as found, in order) with the
+// ordering's buckets.
 __host__ __device__ constexpr size_t topk_smem(int slots, int groups, int cap) {
-  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * 24 + kBuckets * 4;
+  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * (sizeof(Hit) + 16) + kBuckets * 4;
 }
 
-template <typename T, int WARPS, int NV, bool FINE>
+template <typename T, int WARPS, int NV, int GPT>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     topk_stream(TopkArgs a, int64_t rows, int chunks, int per, int cap) {
   using S = Slot<T>;
   using M = NanMax<T>;
-  using Sh = TopkShape<WARPS, NV, FINE>;
+  using Sh = TopkShape<WARPS, NV, GPT>;
   constexpr int N = S::N, kThreads = WARPS * 32, kLanes = Sh::kLanes, kWorkers = Sh::kWorkers;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint32_t scan[33];
@@ -366,13 +697,14 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   __shared__ float part_m[2][32], part_s[2][32];  // [kWorkers]: the row's ends
   __shared__ float bound_sh;
   __shared__ int lo_sh;
-  __shared__ int count[2];
+  __shared__ int count;
   __shared__ int again;
   __shared__ __align__(8) uint64_t full;
   uint4* buf = reinterpret_cast<uint4*>(smem);
   uint32_t* groups = reinterpret_cast<uint32_t*>(buf + Sh::kCap);
-  uint32_t* lists = groups + Sh::kGroups;  // keys, positions; keys, positions
-  uint32_t* order = lists + 4 * cap;       // keys, positions, buckets
+  Hit* hits = reinterpret_cast<Hit*>(groups + Sh::kGroups);
+  uint32_t* found = reinterpret_cast<uint32_t*>(hits + cap);  // keys, positions
+  uint32_t* order = found + 2 * cap;                          // keys, positions, buckets
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int vocab = a.vocab;
   const float c = a.c;
@@ -380,7 +712,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
 
   if (tid == 0) {
     mbar_init(&full, 1);
-    count[0] = count[1] = again = 0;
+    count = again = 0;
     fence_bulk();
   }
   if (warp < kWorkers) {
@@ -391,64 +723,36 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   __syncthreads();
   pdl_wait();
 
-  // adds a candidate
-  auto push = [&](int turn, float f, int at) {
-    const int i = atomicAdd(&count[turn], 1);
-    if (i < cap) {
-      lists[turn * 2 * cap + i] = order_key(f);
-      lists[turn * 2 * cap + cap + i] = (uint32_t)at;
-    }
-  };
-
   if (warp < kWorkers) {
     int turn = 0;
     for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
-      typename M::P group[FINE ? NV : 1];
+      typename M::P group[GPT];
 #pragma unroll
-      for (int v = 0; v < (FINE ? NV : 1); ++v) group[v] = M::none();
+      for (int v = 0; v < GPT; ++v) group[v] = M::none();
       float run = kNegInf, s = 0.0f;  // the warp's maximum below the bound, the lane's sum
       for (int ch = 0; ch < chunks; ++ch) {
         bar_sync(kReady, kThreads - 32);
         const int lo = lo_sh;  // position of the chunk's first element
         uint4 raw[NV];
-        typename M::P top[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           raw[v] = buf[v * kLanes + tid];
-          top[v] = M::slot(raw[v]);
-          if (FINE) {
-            group[v] = M::of(group[v], top[v]);
-            groups[v * kLanes + tid] = order_key(M::value(group[v]));
-          } else {
-            group[0] = M::of(group[0], top[v]);
-          }
+          group[v / (NV / GPT)] = M::of(group[v / (NV / GPT)], M::slot(raw[v]));
         }
-        if (!FINE) groups[tid] = order_key(M::value(group[0]));
+#pragma unroll
+        for (int q = 0; q < GPT; ++q)
+          groups[q * kLanes + tid] = order_key(M::value(group[q]));
         __syncwarp();
         bar_arrive(kMaxima, kThreads - 32);
         bar_sync(kBound, kThreads - 32);
         const float t = bound_sh;
+        const Above<T> above(t);
         SlotMax<T> below;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          if (M::reaches(top[v], t)) {
-            float2 f[N / 2];
-            S::unpack(raw[v], f);
-            uint32_t bits = 0;
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              if (!((e & 1 ? f[e / 2].y : f[e / 2].x) < t)) bits |= 1u << e;
-            const int at = lo + (v * kLanes + tid) * N;
-            for (uint32_t left = bits; left != 0; left &= left - 1) {
-              const int e = __ffs(left) - 1;
-              float x = f[0].x;
-#pragma unroll
-              for (int q = 1; q < N; ++q)
-                if (q == e) x = q & 1 ? f[q / 2].y : f[q / 2].x;
-              push(turn, x, at + e);
-            }
-            S::mask(raw[v], bits);
-          }
+          const uint4 was = raw[v];
+          const uint32_t some = above.take(raw[v]);
+          push_hit(some != 0, was, lo + (v * kLanes + tid) * N, t, &count, hits, cap);
           below.add(raw[v]);
         }
         const float m = warp_max(fmaxf(run, below.get())), ref = finite_ref(m);
@@ -482,18 +786,26 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     // ------------------------------------------------ copies and bounds
     bool lost = false;
     uint32_t phase = 0;
-    const auto start = [&](int64_t row, int ch) {
-      const T* x = static_cast<const T*>(a.logits) + row * a.stride;
-      const RowShape shape = S::shape(x, vocab);
-      const int lo = min(ch * per, shape.slots), held = min(per, shape.slots - lo);
-      if (lane == 0 && !lost) {
-        mbar_expect(&full, (uint32_t)held * 16);
-        if (held > 0)
-          bulk_copy(buf, reinterpret_cast<const uint4*>(x + shape.head) + lo, (uint32_t)held * 16,
-                    &full);
-      }
+    // where a chunk lies, and how many slots it has
+    struct Piece {
+      const T* at;
+      int first, held;  // position of its first element; slots
     };
-    if ((int64_t)blockIdx.x < rows) start(blockIdx.x, 0);
+    const auto piece = [&](int64_t row, int ch) {
+      const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+      const RowShape sh = S::shape(x, vocab);
+      const int lo = min(ch * per, sh.slots);
+      return Piece{x + sh.head + (int64_t)lo * N, sh.head + lo * N, min(per, sh.slots - lo)};
+    };
+    const auto start = [&](const Piece& p) {
+      if (lane == 0) {
+        mbar_expect(&full, (uint32_t)p.held * 16);
+        if (p.held > 0) bulk_copy(buf, p.at, (uint32_t)p.held * 16, &full);
+      }
+      __syncwarp();
+    };
+    Piece now = piece(blockIdx.x, 0);  // (the grid is at most the number of rows)
+    start(now);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
       const T* x = static_cast<const T*>(a.logits) + row * a.stride;
@@ -505,38 +817,32 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         if (!lost && !mbar_wait(&full, phase)) lost = true;
         phase ^= 1;
         lost = __any_sync(kFull, lost);
-        const int lo = min(ch * per, shape.slots), held = min(per, shape.slots - lo);
         // slots past the chunk: -Inf, where another chunk or row had elements
-        for (int q = held + lane; q < per; q += 32) buf[q] = S::none();
-        if (lane == 0) lo_sh = shape.head + lo * N;
-        if (ch == 0 && row != (int64_t)blockIdx.x && row != (int64_t)blockIdx.x + step) {
-          // the list was the row's before the last one: wait until its packet is made
-          __syncwarp();
-          bar_sync(kListFree, 64);
+        if (now.held < per) {
+          for (int q = now.held + lane; q < per; q += 32) buf[q] = S::none();
+          fence_bulk();
         }
-        if (ch == 0 && lane == 0) count[turn] = 0;
+        if (lane == 0) lo_sh = now.first;
         __syncwarp();
         bar_sync(kReady, kThreads - 32);
-        bar_sync(kMaxima, kThreads - 32);
-        // the chunk is in registers
         const bool more = ch + 1 < chunks || row + step < rows;
-        if (more) {
-          fence_bulk();
-          __syncwarp();
-          if (ch + 1 < chunks) start(row, ch + 1);
-          else start(row + step, 0);
-          __syncwarp();
-        }
-        const uint32_t key = a.k > 0 ? warp_bound(groups, Sh::kGroups, a.k) : 0xFFFFFFFFu;
-        // -Inf itself is never a candidate
-        const float lowest = sizeof(T) == 2 && to_f32(from_f32<T>(1e30f)) > 1e38f ? -65504.0f
-                                                                               : -3.402823466e38f;
-        const float t = a.k == 0 ? __int_as_float(0x7F800000) : key == 0 ? lowest : key_value(key);
+        if (more) now = ch + 1 < chunks ? piece(row, ch + 1) : piece(row + step, 0);
+        bar_sync(kMaxima, kThreads - 32);
+        if (more && !lost) start(now);  // the chunk is in registers
+        constexpr int kRegs = Sh::kGroups / 32 <= 16 ? Sh::kGroups / 32 : 0;
+        const uint32_t key = a.k > 0 ? keys_bound<kRegs>(groups, Sh::kGroups, a.k) : 0u;
+        const float t = bound_value<T>(key, a.k);
         if (lane == 0) bound_sh = t;
+        __syncwarp();
+        // the list is free again once the last row's candidates are out of it
+        if (ch == 0 && row != (int64_t)blockIdx.x) bar_sync(kListFree, 64);
+        bar_sync(kBound, kThreads - 32);
         if (ch == 0) {
           const float f = to_f32(edge);
           const bool take = has_edge && f != kNegInf && a.k > 0 && !(f < t);
-          if (take) push(turn, f, edge_at);
+          uint4 raw = S::none();
+          reinterpret_cast<T*>(&raw)[0] = edge;
+          push_hit(take, raw, edge_at, t, &count, hits, cap);
           const float e = take ? kNegInf : f;
           const float m = warp_max(e);
           const float s = warp_sum(exp2_fast((e - finite_ref(m)) * c));
@@ -545,11 +851,9 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
             part_s[turn][kWorkers] = s;
           }
         }
-        __syncwarp();
-        bar_sync(kBound, kThreads - 32);
       }
       __syncwarp();
-      if (lost && lane == 0) count[turn] = cap + 1;
+      if (lost && lane == 0) atomicAdd(&count, cap + 1);
       __syncwarp();
       bar_arrive(kSummed + turn, kThreads);
     }
@@ -558,24 +862,30 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     int turn = 0;
     for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
       bar_sync(kSummed + turn, kThreads);
-      const int n = count[turn];
+      const int slots = count;
+      int32_t* at = reinterpret_cast<int32_t*>(found + cap);
+      const int n = slots <= cap ? warp_candidates<T>(hits, slots, found, at, cap) : cap + 1;
+      const float mw = lane <= kWorkers ? part_m[turn][lane] : kNegInf;
+      const float sw = lane <= kWorkers ? part_s[turn][lane] : 0.0f;
+      __syncwarp();
+      if (lane == 0) count = 0;
+      __syncwarp();
+      if (row + step < rows) bar_arrive(kListFree, 64);
       if (n > cap) {
         if (lane == 0) {
           a.counts[row] = -1;
           again = 1;
         }
-      } else {
-        const float mw = lane <= kWorkers ? part_m[turn][lane] : kNegInf;
-        const float sw = lane <= kWorkers ? part_s[turn][lane] : 0.0f;
-        const float m = warp_max(mw), ref = finite_ref(m);
-        const float s = warp_sum(mw == kNegInf ? sw : sw * exp2_fast((mw - ref) * c));
-        uint32_t* list = lists + turn * 2 * cap;
-        warp_emit(a, row, n, list, reinterpret_cast<int32_t*>(list + cap), order,
-                  reinterpret_cast<int32_t*>(order + cap), order + 2 * cap, m, s);
+        __syncwarp();
+        continue;
       }
+      const float m = warp_max(mw), ref = finite_ref(m);
+      const float s = warp_sum(mw == kNegInf ? sw : sw * exp2_fast((mw - ref) * c));
+      int32_t* at2 = reinterpret_cast<int32_t*>(order + cap);
+      if (n <= 128) warp_emit_few<4>(a, row, n, found, at, order + 2 * cap, at2, m, s);
+      else if (n <= 512) warp_emit_few<16>(a, row, n, found, at, order + 2 * cap, at2, m, s);
+      else warp_emit(a, row, n, found, at, order, at2, order + 2 * cap, m, s);
       __syncwarp();
-      // (for the row after the next one, where there is one)
-      if (row + 2 * step < rows) bar_arrive(kListFree, 64);
     }
   }
   __syncthreads();
@@ -588,6 +898,250 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Short rows: a warp takes one after another, the next one on its way to
+// shared memory.  A slot is a group; the candidates are found in order of their
+// positions, so the packet needs no sorting.
+// ---------------------------------------------------------------------------
+
+constexpr int kShortWarps = 4;  // per CTA
+
+__host__ __device__ constexpr size_t short_smem(int slots, int cap) {
+  return (size_t)slots * 16 + (size_t)cap * 8;
+}
+
+// The packet of n candidates in ascending order of position.
+__device__ __forceinline__ void warp_emit_sorted(const TopkArgs& a, int64_t row, int n,
+                                                 const uint32_t* key, const int32_t* idx, float m,
+                                                 float s) {
+  const int lane = (int)lane_id(), k = a.k;
+  uint32_t cut = 0;  // everything
+  int ties = n;      // keys equal to the cut that belong to the packet
+  if (n > k && k > 0) {
+    uint32_t hi = 0, lo = 0xFFFFFFFFu, any = 0, all = 0xFFFFFFFFu;
+    for (int i = lane; i < n; i += 32) {
+      const uint32_t q = key[i];
+      hi = max(hi, q);
+      lo = min(lo, q);
+      any |= q;
+      all &= q;
+    }
+    hi = __reduce_max_sync(kFull, hi);
+    lo = __reduce_min_sync(kFull, lo);
+    cut = lo;
+    int at = n;
+    if (hi != lo) {
+      const int top = 31 - __clz(hi ^ lo);
+      // bits below `end` are the same in every key (a narrow type's)
+      const int end =
+          __ffs(__reduce_or_sync(kFull, any) & ~__reduce_and_sync(kFull, all)) - 1;
+      cut = lo & ~((2u << top) - 1u);
+      for (int b = top; b >= end && at != k; --b) {
+        const uint32_t mid = cut | (1u << b);
+        int c = 0;
+        for (int i = lane; i < n; i += 32) c += key[i] >= mid ? 1 : 0;
+        c = __reduce_add_sync(kFull, c);
+        if (c >= k) {
+          cut = mid;
+          at = c;
+        }
+      }
+      cut = max(cut | (lo & ((1u << end) - 1u)), lo);
+    }
+    if (at != k) {
+      int above = 0;
+      for (int i = lane; i < n; i += 32) above += key[i] > cut ? 1 : 0;
+      ties = k - __reduce_add_sync(kFull, above);
+    }
+  }
+  const int want = min(k, n);
+  int out = 0, seen = 0;
+  float m2 = kNegInf;  // candidates that are left out
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t q = i < n ? key[i] : 0u;
+    const unsigned same = __ballot_sync(kFull, i < n && q == cut);
+    const bool take = i < n && k > 0 &&
+                      (q > cut || (q == cut && seen + __popc(same & lanemask_lt()) < ties));
+    const unsigned who = __ballot_sync(kFull, take);
+    if (take) {
+      const int to = out + __popc(who & lanemask_lt());
+      a.values[row * k + to] = key_value(q);
+      a.indices[row * k + to] = idx[i];
+    } else if (i < n) {
+      m2 = fmaxf(m2, key_value(q));
+    }
+    out += __popc(who);
+    seen += __popc(same);
+  }
+  for (int j = want + lane; j < k; j += 32) {
+    a.values[row * k + j] = 0.0f;
+    a.indices[row * k + j] = -1;
+  }
+  if (lane == 0) a.counts[row] = want;
+  if (a.tail == nullptr) return;
+  m2 = fmaxf(warp_max(m2), m);
+  const float ref = finite_ref(m2);
+  float s2 = 0.0f;
+  seen = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t q = i < n ? key[i] : 0u;
+    const unsigned same = __ballot_sync(kFull, i < n && q == cut);
+    const bool take = i < n && k > 0 &&
+                      (q > cut || (q == cut && seen + __popc(same & lanemask_lt()) < ties));
+    if (i < n && !take) s2 += exp2_fast((key_value(q) - ref) * a.c);
+    seen += __popc(same);
+  }
+  s2 = warp_sum(s2);
+  s2 += m != kNegInf ? s * exp2_fast((m - ref) * a.c) : s;  // (s is 0, or NaN)
+  if (lane == 0) a.tail[row] = s2 == 0.0f ? kNegInf : fmaf(ref, a.inv_tau, log2_fast(s2) * kLn2);
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kShortWarps * 32, 8)
+    topk_short(TopkArgs a, int64_t rows, int cap) {
+  using S = Slot<T>;
+  using M = NanMax<T>;
+  constexpr int N = S::N;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ uint32_t scan[33];
+  __shared__ float red[32];
+  __shared__ int again;
+  const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  unsigned char* base = smem + (size_t)warp * short_smem(32 * NV, cap);
+  uint4* buf = reinterpret_cast<uint4*>(base);
+  uint32_t* key = reinterpret_cast<uint32_t*>(buf + 32 * NV);
+  int32_t* idx = reinterpret_cast<int32_t*>(key + cap);
+  const int vocab = a.vocab, k = a.k;
+  const float c = a.c;
+  const int64_t step = (int64_t)gridDim.x * kShortWarps;
+  const int64_t first = (int64_t)blockIdx.x * kShortWarps;
+  if (threadIdx.x == 0) again = 0;
+  __syncthreads();
+  pdl_wait();
+
+  T edge_next = from_f32<T>(kNegInf);
+  const auto fetch = [&](int64_t row) {
+    const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+    const RowShape sh = S::shape(x, vocab);
+    const uint4* src = reinterpret_cast<const uint4*>(x + sh.head);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v * 32 + lane < sh.slots) copy_async16(buf + v * 32 + lane, src + v * 32 + lane);
+    if (lane < sh.edge) edge_next = x[S::edge_at(sh, lane)];
+  };
+  if (first + warp < rows) fetch(first + warp);
+  for (int64_t row = first + warp; row < rows; row += step) {
+    const RowShape sh = S::shape(static_cast<const T*>(a.logits) + row * a.stride, vocab);
+    const bool has_edge = lane < sh.edge;
+    float edge = has_edge ? to_f32(edge_next) : kNegInf;
+    copy_async_wait();
+    __syncwarp();
+    uint4 raw[NV];
+    uint32_t top[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      raw[v] = v * 32 + lane < sh.slots ? buf[v * 32 + lane] : S::none();
+      top[v] = order_key(M::value(M::slot(raw[v])));
+    }
+    __syncwarp();
+    if (row + step < rows) fetch(row + step);
+    uint32_t bound = 0;
+    if (k > 0)
+      bound = warp_bound(
+          [&](auto f) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) f(top[v]);
+          },
+          k, k + k / 4 + 4);
+    const float t = bound_value<T>(bound, k);
+    const Above<T> above(t);
+
+    // candidates, in order of position: the row's first elements, its slots, its
+    // last elements
+    int n = 0;
+    const auto append = [&](bool some, float x, int at) {
+      const unsigned who = __ballot_sync(kFull, some);
+      const int to = n + __popc(who & lanemask_lt());
+      if (some && to < cap) {
+        key[to] = order_key(x);
+        idx[to] = at;
+      }
+      n += __popc(who);
+    };
+    const bool edge_in = has_edge && edge != kNegInf && k > 0 && !(edge < t);
+    const bool at_head = lane < sh.head;
+    append(edge_in && at_head, edge, lane);
+    SlotMax<T> below;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint4 was = raw[v];
+      const bool some = above.take(raw[v]) != 0;
+      below.add(raw[v]);
+      const unsigned who = __ballot_sync(kFull, some);
+      if (who != 0) {
+        float2 f[N / 2];
+        S::unpack(was, f);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          bits |= !((e & 1 ? f[e / 2].y : f[e / 2].x) < t) ? 1u << e : 0u;
+        const uint32_t mine = __popc(bits);
+        const uint32_t before = __any_sync(kFull, mine > 1) ? warp_incl_scan(mine) - mine
+                                                            : __popc(who & lanemask_lt());
+        int to = n + (int)before;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (bits >> e & 1u) {
+            if (to < cap) {
+              key[to] = order_key(e & 1 ? f[e / 2].y : f[e / 2].x);
+              idx[to] = sh.head + (v * 32 + lane) * N + e;
+            }
+            ++to;
+          }
+        n += (int)__reduce_add_sync(kFull, mine);
+      }
+    }
+    append(edge_in && !at_head, edge, S::edge_at(sh, lane));
+    if (edge_in) edge = kNegInf;
+    const float m = warp_max(fmaxf(below.get(), edge)), ref = finite_ref(m);
+    float2 sum = make_float2(exp2_fast((edge - ref) * c), 0.0f);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float2 f[N / 2];
+      S::add(raw[v], -ref, f);
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) {
+        f[e] = mul2(f[e], make_float2(c, c));
+        f[e].x = exp2_fast(f[e].x);
+        f[e].y = exp2_fast(f[e].y);
+        sum = add2(sum, f[e]);
+      }
+    }
+    const float s = warp_sum(sum.x + sum.y);
+    __syncwarp();
+    if (n > cap) {
+      if (lane == 0) {
+        a.counts[row] = -1;
+        again = 1;
+      }
+    } else {
+      warp_emit_sorted(a, row, n, key, idx, m, s);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (!again) return;
+  for (int64_t at = first; at < rows; at += step)
+    for (int64_t row = at; row < at + kShortWarps && row < rows; ++row) {
+      const int n = a.counts[row];
+      __syncthreads();
+      if (n == -1) plain_row<T>(a, row, scan, red);
+      __syncthreads();
+    }
+}
+
 // CTAs of a persistent kernel: as many as fit the device, at most `most`.
 int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
   int fit = (int)(225 * 1024 / (smem + 2048));
@@ -596,19 +1150,23 @@ int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
   return (int64_t)sms * fit < most ? (int64_t)sms * fit : most;
 }
 
-template <typename T, int WARPS, int NV, bool FINE>
+template <typename T, int WARPS, int NV, int GPT>
 void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
-  using Sh = TopkShape<WARPS, NV, FINE>;
-  const auto kernel = topk_stream<T, WARPS, NV, FINE>;
+  using Sh = TopkShape<WARPS, NV, GPT>;
+  const auto kernel = topk_stream<T, WARPS, NV, GPT>;
   const int64_t slots = a.vocab / Slot<T>::N + 1;
   const int chunks = (int)((slots + Sh::kCap - 1) / Sh::kCap);
   const int per = (int)((slots + chunks - 1) / chunks);
-  // candidates: about 1.1 k in a row's first chunk, 1.1 k / i in its i-th
-  int deep = 4;
-  while ((1 << (deep - 2)) < chunks) ++deep;
-  int64_t cap = (int64_t)a.k * deep + 512;
+  // candidates: about 1.2 k in a row's first chunk, 1.2 k / i in its i-th
+  float deep = 1.0f;
+  for (int i = 1; i <= chunks && i <= 64; ++i) deep += 1.2f / (float)i;
+  int64_t cap = (int64_t)(deep * (float)a.k) + 256;
+  // in short rows the bound leaves more of them
+  if (cap < 1024 && slots < 1024) cap = 1024;
   if (cap > a.vocab) cap = a.vocab;
-  if (cap > 4096) cap = 4096;
+  const int64_t room = (216 * 1024 - (int64_t)topk_smem(Sh::kCap, Sh::kGroups, 0)) /
+                       (int64_t)(sizeof(Hit) + 16);
+  if (cap > room) cap = room;
   cap = (cap + 3) & ~3;
   const size_t smem = topk_smem(Sh::kCap, Sh::kGroups, (int)cap);
   if (smem > 48 * 1024)
@@ -618,18 +1176,36 @@ void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
              (int)cap);
 }
 
+template <typename T, int NV>
+void launch_short(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
+  const int64_t slots = a.vocab / Slot<T>::N + 1;
+  // little more than k candidates while there are many more groups (slots) than
+  // that; up to all elements otherwise
+  int64_t cap = 3 * (int64_t)a.k > slots ? a.vocab : 4 * (int64_t)a.k + 96;
+  if (cap > a.vocab) cap = a.vocab;
+  cap = (cap + 3) & ~3;
+  const size_t smem = kShortWarps * short_smem(32 * NV, (int)cap);
+  const auto kernel = topk_short<T, NV>;
+  if (smem > 48 * 1024)
+    (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int64_t grid = resident(sms, 8, smem, (rows + kShortWarps - 1) / kShortWarps);
+  launch_pdl(kernel, dim3((unsigned)grid), dim3(kShortWarps * 32), smem, s, a, rows, (int)cap);
+}
+
 template <typename T>
 void launch_typed(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   const int64_t slots = a.vocab / Slot<T>::N + 1;
-  // threads as groups while there are well over k of them
-  if (slots <= TopkShape<4, 8, true>::kCap && a.k <= 256)
-    launch_stream<T, 4, 8, true>(a, rows, sms, s);
-  else if (slots <= TopkShape<8, 8, true>::kCap)
-    launch_stream<T, 8, 8, true>(a, rows, sms, s);
-  else if (a.k <= TopkShape<16, 9, false>::kGroups * 6 / 10)
-    launch_stream<T, 16, 9, false>(a, rows, sms, s);
-  else
-    launch_stream<T, 16, 9, true>(a, rows, sms, s);
+  if (slots <= 32) launch_short<T, 1>(a, rows, sms, s);
+  else if (slots <= 64) launch_short<T, 2>(a, rows, sms, s);
+  else if (slots <= 128) launch_short<T, 4>(a, rows, sms, s);
+  else if (slots <= 256) launch_short<T, 8>(a, rows, sms, s);
+  // several times as many groups as k, where there can be
+  else if (slots <= TopkShape<4, 8, 8>::kCap && a.k <= 256)
+    launch_stream<T, 4, 8, 8>(a, rows, sms, s);
+  else if (slots <= TopkShape<8, 8, 8>::kCap) launch_stream<T, 8, 8, 8>(a, rows, sms, s);
+  else if (a.k <= 128) launch_stream<T, 16, 9, 1>(a, rows, sms, s);
+  else if (a.k <= 384) launch_stream<T, 16, 9, 3>(a, rows, sms, s);
+  else launch_stream<T, 16, 9, 9>(a, rows, sms, s);
 }
 
 }  // namespace
