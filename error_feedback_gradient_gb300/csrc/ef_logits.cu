@@ -196,12 +196,7 @@ __device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
     }
     t = max(t, lo);
   }
-  // the smallest key that is at or above it: a value of the row
-  uint32_t snap = 0xFFFFFFFFu;
-  each([&](uint32_t q) {
-    if (q >= t) snap = min(snap, q);
-  });
-  return __reduce_min_sync(kFull, snap);
+  return t;
 }
 
 // The bound over keys in shared memory, REGS of them per lane in registers; 0:
@@ -209,7 +204,7 @@ __device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
 template <int REGS>
 __device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int k) {
   const int lane = (int)lane_id();
-  const int most = k + k / 4 + 8;
+  const int most = k + k / 8 + 4;
   if constexpr (REGS > 0) {
     uint32_t own[REGS];
 #pragma unroll
@@ -236,10 +231,14 @@ __device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int 
   }
 }
 
-// The value a bound stands for; -Inf itself is never a candidate.
+// The value a bound stands for, rounded to the logits' type: a value between
+// two of the type's rounds to the upper one (the same elements) or to the lower
+// one (more candidates than needed).  -Inf itself is never a candidate.
 template <typename T>
 __device__ __forceinline__ float bound_value(uint32_t key, int k) {
-  return k == 0 ? __int_as_float(0x7F800000) : key == 0 ? Lowest<T>::value() : key_value(key);
+  if (k == 0) return __int_as_float(0x7F800000);
+  const float t = to_f32(from_f32<T>(key_value(key)));
+  return key == 0 || t == kNegInf ? Lowest<T>::value() : t;
 }
 
 constexpr int kBuckets = 512;
@@ -660,37 +659,42 @@ __device__ __forceinline__ void warp_emit(const TopkArgs& a, int64_t row, int n,
 
 // ---------------------------------------------------------------------------
 // A persistent grid; a CTA takes one row after another, in chunks that its
-// workers hold in registers.  Two more warps: the first has chunks copied to
-// shared memory ahead of time and finds the bound from the workers' maxima, the
-// second makes the packet of one row while the others read the next.  A row of
-// several chunks keeps its maxima, so the bound rises from chunk to chunk.
+// workers hold in registers.  The other warps: one has chunks copied to shared
+// memory ahead of time and finds the bound from the workers' maxima; PACK make
+// the packets, of a row each in turn, while the others read on (a packet of 64
+// takes one warp about 9 k cycles, the workers' part of a row of 30522 bf16
+// logits about 6 k).  A row of several chunks keeps its maxima, so the bound
+// rises from chunk to chunk.
 // GPT: groups per thread (its slots are dealt to them in runs).
 // ---------------------------------------------------------------------------
 
 // (kSummed: two, by turns, so that a row's arrivals never meet the last row's)
 enum TopkBarrier { kReady = 1, kMaxima, kBound, kSummed, kListFree = kSummed + 2 };
 
-template <int WARPS, int NV, int GPT>
+template <int WARPS, int PACK, int NV, int GPT>
 struct TopkShape {
-  static constexpr int kWorkers = WARPS - 2, kLanes = kWorkers * 32, kCap = kLanes * NV;
+  static constexpr int kWorkers = WARPS - 1 - PACK, kLanes = kWorkers * 32, kCap = kLanes * NV;
   static constexpr int kGroups = kLanes * GPT;
   static_assert(NV % GPT == 0, "groups of equal size");
 };
 
 // Shared memory in bytes: the chunk, the groups' keys, `cap` slots with
-// candidates, and `cap` candidates twice (as found, in order) with the
-// ordering's buckets.
-__host__ __device__ constexpr size_t topk_smem(int slots, int groups, int cap) {
-  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * (sizeof(Hit) + 16) + kBuckets * 4;
+// candidates, and per packet warp `cap` candidates twice (as found, in order)
+// with the ordering's buckets.
+__host__ __device__ constexpr size_t topk_smem(int slots, int groups, int cap, int pack) {
+  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * (sizeof(Hit) + 16 * pack) +
+         (size_t)pack * kBuckets * 4;
 }
 
-template <typename T, int WARPS, int NV, int GPT>
+template <typename T, int WARPS, int PACK, int NV, int GPT>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     topk_stream(TopkArgs a, int64_t rows, int chunks, int per, int cap) {
   using S = Slot<T>;
   using M = NanMax<T>;
-  using Sh = TopkShape<WARPS, NV, GPT>;
-  constexpr int N = S::N, kThreads = WARPS * 32, kLanes = Sh::kLanes, kWorkers = Sh::kWorkers;
+  using Sh = TopkShape<WARPS, PACK, NV, GPT>;
+  constexpr int N = S::N, kLanes = Sh::kLanes, kWorkers = Sh::kWorkers;
+  constexpr int kPair = kLanes + 32;         // the workers and one more warp
+  constexpr int kSumThreads = kLanes + 64;  // and two more
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint32_t scan[33];
   __shared__ float red[32];
@@ -703,8 +707,6 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   uint4* buf = reinterpret_cast<uint4*>(smem);
   uint32_t* groups = reinterpret_cast<uint32_t*>(buf + Sh::kCap);
   Hit* hits = reinterpret_cast<Hit*>(groups + Sh::kGroups);
-  uint32_t* found = reinterpret_cast<uint32_t*>(hits + cap);  // keys, positions
-  uint32_t* order = found + 2 * cap;                          // keys, positions, buckets
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int vocab = a.vocab;
   const float c = a.c;
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       for (int v = 0; v < GPT; ++v) group[v] = M::none();
       float run = kNegInf, s = 0.0f;  // the warp's maximum below the bound, the lane's sum
       for (int ch = 0; ch < chunks; ++ch) {
-        bar_sync(kReady, kThreads - 32);
+        bar_sync(kReady, kPair);
         const int lo = lo_sh;  // position of the chunk's first element
         uint4 raw[NV];
 #pragma unroll
@@ -743,8 +745,8 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         for (int q = 0; q < GPT; ++q)
           groups[q * kLanes + tid] = order_key(M::value(group[q]));
         __syncwarp();
-        bar_arrive(kMaxima, kThreads - 32);
-        bar_sync(kBound, kThreads - 32);
+        bar_arrive(kMaxima, kPair);
+        bar_sync(kBound, kPair);
         const float t = bound_sh;
         const Above<T> above(t);
         SlotMax<T> below;
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         part_s[turn][warp] = s;
       }
       __syncwarp();
-      bar_arrive(kSummed + turn, kThreads);
+      bar_arrive(kSummed + turn, kSumThreads);
     }
   } else if (warp == kWorkers) {
     // ------------------------------------------------ copies and bounds
@@ -824,10 +826,10 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         }
         if (lane == 0) lo_sh = now.first;
         __syncwarp();
-        bar_sync(kReady, kThreads - 32);
+        bar_sync(kReady, kPair);
         const bool more = ch + 1 < chunks || row + step < rows;
         if (more) now = ch + 1 < chunks ? piece(row, ch + 1) : piece(row + step, 0);
-        bar_sync(kMaxima, kThreads - 32);
+        bar_sync(kMaxima, kPair);
         if (more && !lost) start(now);  // the chunk is in registers
         constexpr int kRegs = Sh::kGroups / 32 <= 16 ? Sh::kGroups / 32 : 0;
         const uint32_t key = a.k > 0 ? keys_bound<kRegs>(groups, Sh::kGroups, a.k) : 0u;
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         __syncwarp();
         // the list is free again once the last row's candidates are out of it
         if (ch == 0 && row != (int64_t)blockIdx.x) bar_sync(kListFree, 64);
-        bar_sync(kBound, kThreads - 32);
+        bar_sync(kBound, kPair);
         if (ch == 0) {
           const float f = to_f32(edge);
           const bool take = has_edge && f != kNegInf && a.k > 0 && !(f < t);
@@ -855,15 +857,20 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       __syncwarp();
       if (lost && lane == 0) atomicAdd(&count, cap + 1);
       __syncwarp();
-      bar_arrive(kSummed + turn, kThreads);
+      bar_arrive(kSummed + turn, kSumThreads);
     }
   } else {
     // ------------------------------------------------ packets
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
-      bar_sync(kSummed + turn, kThreads);
+    const int mine = warp - kWorkers - 1;
+    uint32_t* found = reinterpret_cast<uint32_t*>(hits + cap) + mine * (4 * cap + kBuckets);
+    int32_t* at = reinterpret_cast<int32_t*>(found + cap);  // keys, positions
+    uint32_t* order = found + 2 * cap;                      // keys, positions, buckets
+    int32_t* at2 = reinterpret_cast<int32_t*>(order + cap);
+    int64_t number = mine;  // of the row among the CTA's
+    for (int64_t row = blockIdx.x + mine * step; row < rows; row += PACK * step, number += PACK) {
+      const int turn = (int)(number & 1);
+      bar_sync(kSummed + turn, kSumThreads);
       const int slots = count;
-      int32_t* at = reinterpret_cast<int32_t*>(found + cap);
       const int n = slots <= cap ? warp_candidates<T>(hits, slots, found, at, cap) : cap + 1;
       const float mw = lane <= kWorkers ? part_m[turn][lane] : kNegInf;
       const float sw = lane <= kWorkers ? part_s[turn][lane] : 0.0f;
@@ -881,7 +888,6 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       }
       const float m = warp_max(mw), ref = finite_ref(m);
       const float s = warp_sum(mw == kNegInf ? sw : sw * exp2_fast((mw - ref) * c));
-      int32_t* at2 = reinterpret_cast<int32_t*>(order + cap);
       if (n <= 128) warp_emit_few<4>(a, row, n, found, at, order + 2 * cap, at2, m, s);
       else if (n <= 512) warp_emit_few<16>(a, row, n, found, at, order + 2 * cap, at2, m, s);
       else warp_emit(a, row, n, found, at, order, at2, order + 2 * cap, m, s);
@@ -1150,25 +1156,29 @@ int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
   return (int64_t)sms * fit < most ? (int64_t)sms * fit : most;
 }
 
-template <typename T, int WARPS, int NV, int GPT>
+template <typename T, int WARPS, int PACK, int NV, int GPT>
 void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
-  using Sh = TopkShape<WARPS, NV, GPT>;
-  const auto kernel = topk_stream<T, WARPS, NV, GPT>;
+  using Sh = TopkShape<WARPS, PACK, NV, GPT>;
+  const auto kernel = topk_stream<T, WARPS, PACK, NV, GPT>;
   const int64_t slots = a.vocab / Slot<T>::N + 1;
   const int chunks = (int)((slots + Sh::kCap - 1) / Sh::kCap);
   const int per = (int)((slots + chunks - 1) / chunks);
-  // candidates: about 1.2 k in a row's first chunk, 1.2 k / i in its i-th
-  float deep = 1.0f;
-  for (int i = 1; i <= chunks && i <= 64; ++i) deep += 1.2f / (float)i;
-  int64_t cap = (int64_t)(deep * (float)a.k) + 256;
-  // in short rows the bound leaves more of them
-  if (cap < 1024 && slots < 1024) cap = 1024;
+  // candidates: c groups of G at or above the bound mean -G ln(1 - c / G) of a
+  // first chunk's elements, and a 1 / i-th of that in the i-th
+  const int64_t groups = slots < Sh::kGroups ? slots : Sh::kGroups;
+  const double c = 1.125 * a.k + 4;
+  int64_t cap = a.vocab;
+  if (c < 0.8 * (double)groups) {
+    double chunk_sum = 0.0;
+    for (int i = 1; i <= chunks && i <= 64; ++i) chunk_sum += 1.0 / i;
+    cap = (int64_t)(-(double)groups * std::log(1.0 - c / (double)groups) * chunk_sum * 1.15) + 96;
+  }
   if (cap > a.vocab) cap = a.vocab;
-  const int64_t room = (216 * 1024 - (int64_t)topk_smem(Sh::kCap, Sh::kGroups, 0)) /
-                       (int64_t)(sizeof(Hit) + 16);
+  const int64_t room = (216 * 1024 - (int64_t)topk_smem(Sh::kCap, Sh::kGroups, 0, PACK)) /
+                       (int64_t)(sizeof(Hit) + 16 * PACK);
   if (cap > room) cap = room;
   cap = (cap + 3) & ~3;
-  const size_t smem = topk_smem(Sh::kCap, Sh::kGroups, (int)cap);
+  const size_t smem = topk_smem(Sh::kCap, Sh::kGroups, (int)cap, PACK);
   if (smem > 48 * 1024)
     (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   const int64_t grid = resident(sms, 32 / WARPS, smem, rows);
@@ -1200,12 +1210,11 @@ void launch_typed(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   else if (slots <= 128) launch_short<T, 4>(a, rows, sms, s);
   else if (slots <= 256) launch_short<T, 8>(a, rows, sms, s);
   // several times as many groups as k, where there can be
-  else if (slots <= TopkShape<4, 8, 8>::kCap && a.k <= 256)
-    launch_stream<T, 4, 8, 8>(a, rows, sms, s);
-  else if (slots <= TopkShape<8, 8, 8>::kCap) launch_stream<T, 8, 8, 8>(a, rows, sms, s);
-  else if (a.k <= 128) launch_stream<T, 16, 9, 1>(a, rows, sms, s);
-  else if (a.k <= 384) launch_stream<T, 16, 9, 3>(a, rows, sms, s);
-  else launch_stream<T, 16, 9, 9>(a, rows, sms, s);
+  else if (slots <= TopkShape<4, 1, 8, 8>::kCap && a.k <= 128)
+    launch_stream<T, 4, 1, 8, 8>(a, rows, sms, s);
+  else if (slots <= TopkShape<8, 1, 8, 8>::kCap) launch_stream<T, 8, 1, 8, 8>(a, rows, sms, s);
+  else if (a.k <= 256) launch_stream<T, 16, 2, 10, 1>(a, rows, sms, s);
+  else launch_stream<T, 16, 2, 10, 10>(a, rows, sms, s);
 }
 
 }  // namespace
