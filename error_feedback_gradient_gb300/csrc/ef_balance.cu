@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCountThreads = 1024;
 constexpr int kSegBatch = 512;  // segments per launch
 constexpr float kLog2e = 1.4426950408889634f;
 // Rounds of eight CTAs' warps up to which one launch with a cluster per segment
@@ -59,41 +60,6 @@ struct BalanceArgs {
   const float* seg_grad;
   void* grad;
   int64_t grad_stride;
-};
-
-// N neighbouring elements as they lie in memory.
-template <typename T, int N>
-struct Cell {
-  using Raw = uint4;
-  static __device__ __forceinline__ Raw load(const T* p) {
-    return __ldcs(reinterpret_cast<const uint4*>(p));
-  }
-  static __device__ __forceinline__ Raw none() { return Slot<T>::none(); }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[N]) {
-    float2 p[N / 2];
-    Slot<T>::unpack(r, p);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      f[2 * i] = p[i].x;
-      f[2 * i + 1] = p[i].y;
-    }
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&f)[N]) {
-    float2 q[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) q[i] = make_float2(f[2 * i], f[2 * i + 1]);
-    __stcs(reinterpret_cast<uint4*>(p), Slot<T>::pack(q));
-  }
-};
-template <typename T>
-struct Cell<T, 1> {
-  using Raw = T;
-  static __device__ __forceinline__ Raw load(const T* p) { return *p; }
-  static __device__ __forceinline__ Raw none() { return from_f32<T>(kNegInf); }
-  static __device__ __forceinline__ void unpack(const Raw& r, float (&f)[1]) { f[0] = to_f32(r); }
-  static __device__ __forceinline__ void store(T* p, const float (&f)[1]) {
-    *p = from_f32<T>(f[0]);
-  }
 };
 
 // Counts the ids of tokens [t0, t1) into `cnt` (shared, E zeroed words) and
@@ -127,6 +93,85 @@ __device__ __forceinline__ int count_tokens(const BalanceArgs& a, int64_t t0, in
   return n;
 }
 
+// A lane's part of a token: NV cells of N neighbouring elements (16 bytes, or
+// one element), cell j at (lane in group) + j G.  Everything after the loads is
+// done on pairs of elements.
+template <typename T, int N, int NV>
+struct Part {
+  using Raw = typename std::conditional<N == 1, T, uint4>::type;
+  static constexpr int kPairs = N * NV / 2;
+  Raw raw[NV];
+
+  __device__ __forceinline__ void load(const T* z, int sub, int G, int cells, bool valid) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int cell = sub + j * G;
+      const bool in = valid && cell < cells;
+      if constexpr (N == 1) {
+        raw[j] = in ? z[cell] : from_f32<T>(kNegInf);
+      } else {
+        raw[j] = Slot<T>::none();
+        if (in) raw[j] = __ldcs(reinterpret_cast<const uint4*>(z) + cell);
+      }
+    }
+  }
+  __device__ __forceinline__ float max() const {
+    if constexpr (N == 1) {
+      float m = kNegInf;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) m = fmaxf(m, to_f32(raw[j]));
+      return m;
+    } else {
+      SlotMax<T> m;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) m.add(raw[j]);
+      return m.get();
+    }
+  }
+  // the elements plus d, in pairs
+  __device__ __forceinline__ void add(float d, float2 (&f)[kPairs]) const {
+    if constexpr (N == 1) {
+#pragma unroll
+      for (int j = 0; j < NV / 2; ++j)
+        f[j] = make_float2(to_f32(raw[2 * j]) + d, to_f32(raw[2 * j + 1]) + d);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float2 q[N / 2];
+        Slot<T>::add(raw[j], d, q);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) f[j * (N / 2) + i] = q[i];
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* g, int sub, int G, int cells,
+                                               const float2 (&f)[kPairs]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int cell = sub + j * G;
+      if (cell >= cells) continue;
+      if constexpr (N == 1) {
+        g[cell] = from_f32<T>(j & 1 ? f[j / 2].y : f[j / 2].x);
+      } else {
+        float2 q[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) q[i] = f[j * (N / 2) + i];
+        __stcs(reinterpret_cast<uint4*>(g) + cell, Slot<T>::pack(q));
+      }
+    }
+  }
+  // f_e at the lane's elements; 0 past the last expert
+  static __device__ __forceinline__ void factors(const float* f_sh, int sub, int G, int cells,
+                                                 float2 (&f)[kPairs]) {
+#pragma unroll
+    for (int q = 0; q < kPairs; ++q) {
+      const int c0 = sub + (2 * q / N) * G, c1 = sub + ((2 * q + 1) / N) * G;
+      f[q].x = c0 < cells ? f_sh[c0 * N + 2 * q % N] : 0.0f;
+      f[q].y = c1 < cells ? f_sh[c1 * N + (2 * q + 1) % N] : 0.0f;
+    }
+  }
+};
+
 // The pass over tokens first, first + step, .. < t1 (`first` per warp: its
 // groups take neighbouring tokens).  Adds d_t and L_t^2 to the lane's sums (lane
 // 0 of each group holds them).
@@ -134,60 +179,45 @@ template <typename T, int N, int NV, bool GRAD>
 __device__ __forceinline__ void pass_tokens(const BalanceArgs& a, int64_t first, int64_t t1,
                                             int64_t step, int G, const float* f_sh, float w,
                                             float* d_sum, float* z_sum) {
-  using C = Cell<T, N>;
+  using P = Part<T, N, NV>;
+  constexpr int kPairs = P::kPairs;
   const int lane = (int)(threadIdx.x & 31), sub = lane & (G - 1), group = lane / G;
   const int cells = a.experts / N;  // (N divides experts)
-  float f[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int cell = sub + j * G;
-      f[j][i] = cell < cells ? f_sh[cell * N + i] : 0.0f;
-    }
-  typename C::Raw raw[NV];
+  float2 f[kPairs];
+  P::factors(f_sh, sub, G, cells, f);
+  P part;
   uint8_t keep = 1;
   const auto load = [&](int64_t t) {
-    const T* z = static_cast<const T*>(a.logits) + t * a.stride;
     keep = t < t1 && a.mask ? a.mask[t] : 1;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int cell = sub + j * G;
-      raw[j] = C::none();
-      if (t < t1 && cell < cells) raw[j] = C::load(z + cell * N);
-    }
+    part.load(static_cast<const T*>(a.logits) + t * a.stride, sub, G, cells, t < t1);
   };
   load(first + group);
   for (int64_t base = first; base < t1; base += step) {
     const int64_t t = base + group;
-    float p[NV][N];
-    float m = kNegInf;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      C::unpack(raw[j], p[j]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, p[j][i]);
-    }
-    const bool on = keep != 0;
-    load(t + step);
+    float m = part.max();
     for (int o = G >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     m = finite_ref(m);
-    float sum = 0.0f, dot = 0.0f;
+    float2 p[kPairs];
+    part.add(-m, p);
+    const bool on = keep != 0;
+    load(t + step);
+    float2 sum2 = make_float2(0.0f, 0.0f), dot2 = sum2;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[j][i] = exp2_fast((p[j][i] - m) * kLog2e);
-        sum += p[j][i];
-        dot = fmaf(p[j][i], f[j][i], dot);
-      }
+    for (int q = 0; q < kPairs; ++q) {
+      p[q] = mul2(p[q], make_float2(kLog2e, kLog2e));
+      p[q].x = exp2_fast(p[q].x);
+      p[q].y = exp2_fast(p[q].y);
+      sum2 = add2(sum2, p[q]);
+      dot2 = fma2(p[q], f[q], dot2);
+    }
+    float sum = sum2.x + sum2.y, dot = dot2.x + dot2.y;
     for (int o = G >> 1; o > 0; o >>= 1) {
       sum += __shfl_xor_sync(kFull, sum, o);
       dot += __shfl_xor_sync(kFull, dot, o);
     }
     // nothing left in the row (sum 0), or padding: p = 0 and no term
     const bool none = sum == 0.0f || !on;
-    const float inv = none ? 0.0f : 1.0f / sum;
+    const float inv = none ? 0.0f : __fdividef(1.0f, sum);
     const float lse = none ? 0.0f : fmaf(log2_fast(sum), kLn2, m);
     dot = none ? 0.0f : dot * inv;
     if (t < t1) {
@@ -199,16 +229,12 @@ __device__ __forceinline__ void pass_tokens(const BalanceArgs& a, int64_t first,
         // p (alpha (f - d) + 2 beta L) w
         const float aw = none ? 0.0f : a.alpha * w * inv;
         const float b = none ? 0.0f : w * inv * (2.0f * a.beta * lse - a.alpha * dot);
-        T* g = static_cast<T*>(a.grad) + t * a.grad_stride;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int cell = sub + j * G;
-          if (cell >= cells) continue;
-          float d[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) d[i] = none ? 0.0f : p[j][i] * fmaf(aw, f[j][i], b);
-          C::store(g + cell * N, d);
+        for (int q = 0; q < kPairs; ++q) {
+          p[q] = mul2(p[q], fma2(f[q], make_float2(aw, aw), make_float2(b, b)));
+          if (none) p[q] = make_float2(0.0f, 0.0f);
         }
+        P::store(static_cast<T*>(a.grad) + t * a.grad_stride, sub, G, cells, p);
       }
     }
   }
@@ -220,20 +246,32 @@ __device__ __forceinline__ float loss_of(const BalanceArgs& a, float d_sum, floa
   return (a.alpha * d_sum + (a.beta != 0.0f ? a.beta * z_sum : 0.0f)) * inv_n;
 }
 
-// Sums of a block's two values, in every thread; the order is fixed.
-__device__ __forceinline__ float2 block_sum2(float2 v, float* scratch) {
-  v.x = block_sum(v.x, scratch);
-  v.y = block_sum(v.y, scratch);
+// Sums of a block's two values, in thread 0; the order is fixed.  `scratch`:
+// kWarps pairs.
+__device__ __forceinline__ float2 block_sum2(float2 v, float2* scratch) {
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  if (lane_id() == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = make_float2(0.0f, 0.0f);
+  if (threadIdx.x < 32) {
+    if (threadIdx.x < kWarps) v = scratch[threadIdx.x];
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+  }
   return v;
 }
 
+// CTAs per SM for a pass with this many elements per lane (its registers).
+constexpr int ctas_for(int elements) { return elements <= 16 ? 4 : elements <= 32 ? 2 : 1; }
+
 // One cluster of CTAs per segment: counts, sums and gradients in one launch.
 template <typename T, int N, int NV, bool GRAD>
-__global__ void __launch_bounds__(kThreads) balance_segment(BalanceArgs a, SegBatch seg, int first,
-                                                            int cluster, int G) {
+__global__ void __launch_bounds__(kThreads, ctas_for(N* NV))
+    balance_segment(BalanceArgs a, SegBatch seg, int first, int cluster, int G) {
   __shared__ int32_t cnt[EF_MAX_EXPERTS];
   __shared__ float f[EF_MAX_EXPERTS];
-  __shared__ float red[32];
+  __shared__ float2 red[kWarps];
   __shared__ int32_t n_tok;
   __shared__ float2 sums;
   const int tid = threadIdx.x, E = a.experts;
@@ -252,11 +290,17 @@ __global__ void __launch_bounds__(kThreads) balance_segment(BalanceArgs a, SegBa
   if (cluster > 1) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    for (int r = 0; r < cluster; ++r) n += *cl.map_shared_rank(&n_tok, r);
+    // (all of a thread's remote loads at once: one after another they were 2 us)
+    const int lane = tid & 31;
+    n = __reduce_add_sync(kFull, lane < cluster ? *cl.map_shared_rank(&n_tok, lane) : 0);
     const float by_n = n > 0 ? scale / (float)n : 0.0f;
     for (int e = tid; e < E; e += kThreads) {
+      int32_t part[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) part[r] = r < cluster ? *cl.map_shared_rank(&cnt[e], r) : 0;
       int32_t c = 0;
-      for (int r = 0; r < cluster; ++r) c += *cl.map_shared_rank(&cnt[e], r);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) c += part[r];
       f[e] = (float)c * by_n;
       if (rank == 0) a.counts[(int64_t)s * E + e] = c;
     }
@@ -280,13 +324,11 @@ __global__ void __launch_bounds__(kThreads) balance_segment(BalanceArgs a, SegBa
     cg::cluster_group cl = cg::this_cluster();
     if (tid == 0) sums = v;
     cl.sync();
-    if (rank == 0 && tid == 0) {
+    if (rank == 0 && tid < 32) {
       v = make_float2(0.0f, 0.0f);
-      for (int r = 0; r < cluster; ++r) {
-        const float2 q = *cl.map_shared_rank(&sums, r);
-        v.x += q.x;
-        v.y += q.y;
-      }
+      if (tid < cluster) v = *cl.map_shared_rank(&sums, tid);
+      v.x = warp_sum(v.x);
+      v.y = warp_sum(v.y);
     }
     cl.sync();
   }
@@ -334,11 +376,11 @@ __device__ __forceinline__ int segment_at(const SegBatch& seg, int64_t t) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) balance_count(BalanceArgs a, SegBatch seg, int64_t t0,
+__global__ void __launch_bounds__(kCountThreads) balance_count(BalanceArgs a, SegBatch seg, int64_t t0,
                                                           int tile) {
   __shared__ int32_t cnt[EF_MAX_EXPERTS];
   __shared__ int32_t n_tok;
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) cnt[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += kCountThreads) cnt[e] = 0;
   if (threadIdx.x == 0) n_tok = 0;
   __syncthreads();
   pdl_wait();
@@ -350,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) balance_count(BalanceArgs a, SegBatc
     const int mine = count_tokens(a, b, e1, cnt);
     if (mine != 0) atomicAdd(&n_tok, mine);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += kThreads) {
+    for (int e = threadIdx.x; e < a.experts; e += kCountThreads) {
       if (cnt[e] != 0) atomicAdd(&a.counts[(int64_t)s * a.experts + e], cnt[e]);
       cnt[e] = 0;
     }
@@ -364,10 +406,10 @@ __global__ void __launch_bounds__(kThreads) balance_count(BalanceArgs a, SegBatc
 
 // `a.counts_in`, `a.tokens_in`, `a.seg_grad`, `a.loss` start at the batch.
 template <typename T, int N, int NV, bool LOSS, bool GRAD>
-__global__ void __launch_bounds__(kThreads) balance_tiles(BalanceArgs a, SegBatch seg, int64_t t0,
-                                                          int tile, int G, TileSums* ts) {
+__global__ void __launch_bounds__(kThreads, ctas_for(N* NV))
+    balance_tiles(BalanceArgs a, SegBatch seg, int64_t t0, int tile, int G, TileSums* ts) {
   __shared__ float f[EF_MAX_EXPERTS];
-  __shared__ float red[32];
+  __shared__ float2 red[kWarps];
   __shared__ bool is_last;
   pdl_wait();
   const int tid = threadIdx.x, E = a.experts;
@@ -389,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) balance_tiles(BalanceArgs a, SegBatc
     pass_tokens<T, N, NV, GRAD>(a, b + (tid >> 5) * per_warp, e1, kWarps * per_warp, G, f, w,
                                 &v.x, &v.y);
     if (LOSS) {
-      v = block_sum2(v, red);
+      v = block_sum2(v, red);  // (the next segment's first barrier ends its reads)
       if (tid == 0) ts->sums[blockIdx.x + s] = v;
     }
   }
@@ -534,10 +576,11 @@ ef_status launch_batch(BalanceArgs a, const SegBatch& seg, int first, int sms, c
   }
   TileSums* ts = LOSS ? reinterpret_cast<TileSums*>(a.ws + 1) : nullptr;
   if (tokens == 0) return EF_OK;  // (a gradient alone: nothing to write)
-  // four CTAs per SM, their tiles whole rounds of the CTA's warps where there
-  // are several of them
+  // as many CTAs as are resident, their tiles whole rounds of the CTA's warps
+  // where there are several of them
   const int round = kWarps * (32 / form.G);
-  int64_t tile = (tokens + 4 * sms - 1) / (4 * sms);
+  const int64_t ctas = (int64_t)sms * ctas_for(form.wide ? form.nv * (16 / (int)sizeof(T)) : form.nv);
+  int64_t tile = (tokens + ctas - 1) / ctas;
   if (tile > 2 * round) tile = (tile + round - 1) / round * round;
   const int64_t least = (tokens + kMaxTiles - 1) / kMaxTiles;
   if (tile < least) tile = least;
@@ -554,7 +597,10 @@ ef_status launch_batch(BalanceArgs a, const SegBatch& seg, int first, int sms, c
                0, s, a, (int)seg.n, ts);
     ef_status st = check_launch();
     if (st != EF_OK) return st;
-    launch_pdl(balance_count, dim3(tiles), dim3(kThreads), 0, s, a, seg, t0, (int)tile);
+    // one CTA per SM: each ends with an addition per expert to the counts
+    const int64_t part = (tokens + sms - 1) / sms;
+    launch_pdl(balance_count, dim3((unsigned)((tokens + part - 1) / part)), dim3(kCountThreads),
+               0, s, a, seg, t0, (int)part);
     st = check_launch();
     if (st != EF_OK) return st;
   } else {
