@@ -62,6 +62,13 @@ struct Lowest<__half> {
   static __device__ __forceinline__ float value() { return -65504.0f; }
 };
 
+// order_key of a group's maximum: canonical NaN or none, and -0 just below +0
+// (a bound between the two takes in both: it is compared as a float).
+__device__ __forceinline__ uint32_t group_key(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
 // The value of a key (a NaN key gives a NaN).
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
@@ -252,6 +259,7 @@ template <>
 struct Above<float> {
   float t;
   __device__ __forceinline__ explicit Above(float x) : t(x) {}
+  __device__ __forceinline__ bool reached(float most) const { return !(most < t); }
   __device__ __forceinline__ uint32_t take(uint4& r) const {
     uint32_t some = 0;
     uint32_t* w = reinterpret_cast<uint32_t*>(&r);
@@ -268,6 +276,9 @@ template <>
 struct Above<__nv_bfloat16> {
   __nv_bfloat162 t;
   __device__ __forceinline__ explicit Above(float x) : t(__float2bfloat162_rn(x)) {}
+  __device__ __forceinline__ bool reached(__nv_bfloat162 most) const {
+    return __hgeu2_mask(most, t) != 0;
+  }
   __device__ __forceinline__ uint32_t take(uint4& r) const {
     uint32_t some = 0;
     uint32_t* w = reinterpret_cast<uint32_t*>(&r);
@@ -284,6 +295,9 @@ template <>
 struct Above<__half> {
   __half2 t;
   __device__ __forceinline__ explicit Above(float x) : t(__float2half2_rn(x)) {}
+  __device__ __forceinline__ bool reached(__half2 most) const {
+    return __hgeu2_mask(most, t) != 0;
+  }
   __device__ __forceinline__ uint32_t take(uint4& r) const {
     uint32_t some = 0;
     uint32_t* w = reinterpret_cast<uint32_t*>(&r);
@@ -297,57 +311,55 @@ struct Above<__half> {
   }
 };
 
-// Slots that hold candidates: their elements, the first one's position and the
-// bound they were held against.
-struct Hit {
-  uint4 raw;
-  int32_t at;
-  float bound;
-  uint32_t pad[2];
-};
-
-// A whole warp appends the slots of its lanes with `some` set.
-__device__ __forceinline__ void push_hit(bool some, const uint4& raw, int at, float t, int* count,
-                                         Hit* hits, int cap) {
-  const unsigned who = __ballot_sync(kFull, some);
-  if (who == 0) return;
-  int base = 0;
-  if (lane_id() == 0) base = atomicAdd(count, __popc(who));
-  base = __shfl_sync(kFull, base, 0) + __popc(who & lanemask_lt());
-  if (some && base < cap) {
-    hits[base].raw = raw;
-    hits[base].at = at;
-    hits[base].bound = t;
+// The list of slots that hold candidates: their elements, the first one's
+// position and the bound they were held against.
+struct Hits {
+  uint4* raw;
+  int32_t* at;
+  float* bound;
+  int cap;
+  __device__ __forceinline__ void put(int i, const uint4& r, int position, float t) const {
+    if (i >= cap) return;
+    raw[i] = r;
+    at[i] = position;
+    bound[i] = t;
   }
-}
+};
+constexpr int kHitBytes = 24;
 
 // The candidates of n slots as keys and positions, in any order; returns their
-// number (more than cap: the rest is not there).
-template <typename T>
-__device__ __forceinline__ int warp_candidates(const Hit* hits, int n, uint32_t* key,
-                                               int32_t* idx, int cap) {
+// number (more than there is room for: the rest is not there).  Elements below t, the last and
+// highest bound, are left out again (AGAIN: there may be such, as a row's bound
+// rises from chunk to chunk): `dropped` is the largest of them.
+template <typename T, bool AGAIN>
+__device__ __forceinline__ int warp_candidates(const Hits& hits, int n, float t, uint32_t* key,
+                                               int32_t* idx, int room, float& dropped) {
   constexpr int N = Slot<T>::N;
   int total = 0;
+  float most = kNegInf;
   for (int h0 = 0; h0 < n; h0 += 32) {
     const int h = h0 + (int)lane_id();
-    const T* e = reinterpret_cast<const T*>(&hits[h].raw);
+    const T* e = reinterpret_cast<const T*>(hits.raw + h);
     uint32_t left = 0;
     int at = 0;
     if (h < n) {
-      const uint4 raw = hits[h].raw;
-      const float t = hits[h].bound;
-      at = hits[h].at;
+      const uint4 raw = hits.raw[h];
+      const float was = hits.bound[h];
+      at = hits.at[h];
       float2 f[N / 2];
       Slot<T>::unpack(raw, f);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        left |= !((i & 1 ? f[i / 2].y : f[i / 2].x) < t) ? 1u << i : 0u;
+      for (int i = 0; i < N; ++i) {
+        const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
+        left |= !(x < t) ? 1u << i : 0u;
+        if (AGAIN && x < t && x >= was) most = fmaxf(most, x);
+      }
     }
     for (unsigned who = __ballot_sync(kFull, left != 0); who != 0;
          who = __ballot_sync(kFull, left != 0)) {
       if (left != 0) {
         const int i = __ffs(left) - 1, to = total + __popc(who & lanemask_lt());
-        if (to < cap) {
+        if (to < room) {
           key[to] = order_key(to_f32(e[i]));
           idx[to] = at + i;
         }
@@ -357,7 +369,30 @@ __device__ __forceinline__ int warp_candidates(const Hit* hits, int n, uint32_t*
     }
   }
   __syncwarp();
+  dropped = AGAIN ? warp_max(most) : kNegInf;
   return total;
+}
+
+// The sum of 2^((x - ref) c) over the elements that warp_candidates left out
+// again, none of them above ref.  As integers, so that the list's order does not
+// matter: 2^-31 of a term of 1 each.
+template <typename T>
+__device__ __noinline__ float warp_dropped(const Hits& hits, int n, float t, float ref, float c) {
+  constexpr int N = Slot<T>::N;
+  unsigned long long sum = 0;
+  for (int h = (int)lane_id(); h < n; h += 32) {
+    const float was = hits.bound[h];
+    float2 f[N / 2];
+    Slot<T>::unpack(hits.raw[h], f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
+      if (x < t && x >= was) sum += __float2uint_rn(exp2_fast((x - ref) * c) * 0x1p30f);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  return (float)sum * 0x1p-30f;
 }
 
 // The packet of at most 32 * PER candidates, which are held in registers.  The
@@ -664,7 +699,13 @@ __device__ __forceinline__ void warp_emit(const TopkArgs& a, int64_t row, int n,
 // the packets, of a row each in turn, while the others read on (a packet of 64
 // takes one warp about 9 k cycles, the workers' part of a row of 30522 bf16
 // logits about 6 k).  A row of several chunks keeps its maxima, so the bound
-// rises from chunk to chunk.
+// rises from chunk to chunk; only the first one is waited for.  Later chunks are
+// held against the bound of the chunks before them while the next one is
+// searched for, and what falls below the last bound is added to the tail by the
+// packet's warp.
+// 8192 rows of 30522 bf16 logits, k 64: 132 us, 3.8 TB/s; two CTAs per SM, each
+// waiting in turn for the bound's search (1.4 k cycles and more), its candidates
+// and the packet warps; the sums' exponentials are 10 us of it.
 // GPT: groups per thread (its slots are dealt to them in runs).
 // ---------------------------------------------------------------------------
 
@@ -679,16 +720,17 @@ struct TopkShape {
 };
 
 // Shared memory in bytes: the chunk, the groups' keys, `cap` slots with
-// candidates, and per packet warp `cap` candidates twice (as found, in order)
+// candidates, and per packet warp `room` candidates twice (as found, in order)
 // with the ordering's buckets.
-__host__ __device__ constexpr size_t topk_smem(int slots, int groups, int cap, int pack) {
-  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * (sizeof(Hit) + 16 * pack) +
-         (size_t)pack * kBuckets * 4;
+__host__ __device__ constexpr size_t topk_smem(int slots, int groups, int cap, int room,
+                                               int pack) {
+  return (size_t)slots * 16 + (size_t)groups * 4 + (size_t)cap * kHitBytes +
+         (size_t)pack * (room * 16 + kBuckets * 4);
 }
 
 template <typename T, int WARPS, int PACK, int NV, int GPT>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
-    topk_stream(TopkArgs a, int64_t rows, int chunks, int per, int cap) {
+    topk_stream(TopkArgs a, int64_t rows, int chunks, int per, int cap, int room) {
   using S = Slot<T>;
   using M = NanMax<T>;
   using Sh = TopkShape<WARPS, PACK, NV, GPT>;
@@ -699,14 +741,19 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   __shared__ uint32_t scan[33];
   __shared__ float red[32];
   __shared__ float part_m[2][32], part_s[2][32];  // [kWorkers]: the row's ends
-  __shared__ float bound_sh;
+  __shared__ float part_t[2];                     // the row's last bound
+  __shared__ float bound_sh;  // of the chunks before, or (a row's first) of the chunk
   __shared__ int lo_sh;
   __shared__ int count;
   __shared__ int again;
   __shared__ __align__(8) uint64_t full;
   uint4* buf = reinterpret_cast<uint4*>(smem);
   uint32_t* groups = reinterpret_cast<uint32_t*>(buf + Sh::kCap);
-  Hit* hits = reinterpret_cast<Hit*>(groups + Sh::kGroups);
+  Hits hits;  // (cap and room: multiples of 4)
+  hits.cap = cap;
+  hits.raw = reinterpret_cast<uint4*>(groups + Sh::kGroups);
+  hits.at = reinterpret_cast<int32_t*>(hits.raw + cap);
+  hits.bound = reinterpret_cast<float*>(hits.at + cap);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int vocab = a.vocab;
   const float c = a.c;
@@ -732,6 +779,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
 #pragma unroll
       for (int v = 0; v < GPT; ++v) group[v] = M::none();
       float run = kNegInf, s = 0.0f;  // the warp's maximum below the bound, the lane's sum
+      float t = 0.0f;
       for (int ch = 0; ch < chunks; ++ch) {
         bar_sync(kReady, kPair);
         const int lo = lo_sh;  // position of the chunk's first element
@@ -745,18 +793,29 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         for (int q = 0; q < GPT; ++q)
           groups[q * kLanes + tid] = order_key(M::value(group[q]));
         __syncwarp();
+        if (ch > 0) t = bound_sh;
+        __syncwarp();
         bar_arrive(kMaxima, kPair);
-        bar_sync(kBound, kPair);
-        const float t = bound_sh;
+        if (ch == 0) {
+          bar_sync(kBound, kPair);
+          t = bound_sh;
+        }
         const Above<T> above(t);
+        uint32_t mine = 0;  // bit v: slot v holds candidates
+#pragma unroll
+        for (int v = 0; v < NV; ++v) mine |= above.reached(M::slot(raw[v])) ? 1u << v : 0u;
+        int to = 0;
+        if (mine != 0) to = atomicAdd(&count, __popc(mine));
         SlotMax<T> below;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const uint4 was = raw[v];
-          const uint32_t some = above.take(raw[v]);
-          push_hit(some != 0, was, lo + (v * kLanes + tid) * N, t, &count, hits, cap);
+          if (mine >> v & 1u) {
+            hits.put(to++, raw[v], lo + (v * kLanes + tid) * N, t);
+            above.take(raw[v]);
+          }
           below.add(raw[v]);
         }
+        __syncwarp();
         const float m = warp_max(fmaxf(run, below.get())), ref = finite_ref(m);
         float2 sum = make_float2(0.0f, 0.0f);
         if (run != kNegInf) sum.x = s * exp2_fast((run - ref) * c);
@@ -786,8 +845,17 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     }
   } else if (warp == kWorkers) {
     // ------------------------------------------------ copies and bounds
-    bool lost = false;
+    bool lost = false;    // a wait ran out: the rows from there on are left to plain_row
+    bool flying = false;  // a copy is under way
     uint32_t phase = 0;
+    const auto land = [&] {  // waits for the copy under way
+      if (flying && __all_sync(kFull, mbar_wait(&full, phase))) {
+        flying = false;
+        phase ^= 1;
+      } else {
+        lost = true;
+      }
+    };
     // where a chunk lies, and how many slots it has
     struct Piece {
       const T* at;
@@ -800,6 +868,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       return Piece{x + sh.head + (int64_t)lo * N, sh.head + lo * N, min(per, sh.slots - lo)};
     };
     const auto start = [&](const Piece& p) {
+      flying = true;
       if (lane == 0) {
         mbar_expect(&full, (uint32_t)p.held * 16);
         if (p.held > 0) bulk_copy(buf, p.at, (uint32_t)p.held * 16, &full);
@@ -815,10 +884,9 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       const bool has_edge = lane < shape.edge;
       const int edge_at = S::edge_at(shape, lane);
       const T edge = has_edge ? x[edge_at] : from_f32<T>(kNegInf);
+      float t = 0.0f;
       for (int ch = 0; ch < chunks; ++ch) {
-        if (!lost && !mbar_wait(&full, phase)) lost = true;
-        phase ^= 1;
-        lost = __any_sync(kFull, lost);
+        land();
         // slots past the chunk: -Inf, where another chunk or row had elements
         if (now.held < per) {
           for (int q = now.held + lane; q < per; q += 32) buf[q] = S::none();
@@ -833,18 +901,20 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         if (more && !lost) start(now);  // the chunk is in registers
         constexpr int kRegs = Sh::kGroups / 32 <= 16 ? Sh::kGroups / 32 : 0;
         const uint32_t key = a.k > 0 ? keys_bound<kRegs>(groups, Sh::kGroups, a.k) : 0u;
-        const float t = bound_value<T>(key, a.k);
-        if (lane == 0) bound_sh = t;
+        // (a search ends early, so a later one may find less)
+        t = ch > 0 ? fmaxf(t, bound_value<T>(key, a.k)) : bound_value<T>(key, a.k);
+        if (lane == 0) bound_sh = part_t[turn] = t;
         __syncwarp();
-        // the list is free again once the last row's candidates are out of it
-        if (ch == 0 && row != (int64_t)blockIdx.x) bar_sync(kListFree, 64);
-        bar_sync(kBound, kPair);
         if (ch == 0) {
+          // the list is free again once the last row's candidates are out of it
+          if (row != (int64_t)blockIdx.x) bar_sync(kListFree, 64);
+          bar_sync(kBound, kPair);
           const float f = to_f32(edge);
           const bool take = has_edge && f != kNegInf && a.k > 0 && !(f < t);
           uint4 raw = S::none();
           reinterpret_cast<T*>(&raw)[0] = edge;
-          push_hit(take, raw, edge_at, t, &count, hits, cap);
+          if (take) hits.put(atomicAdd(&count, 1), raw, edge_at, t);
+          __syncwarp();
           const float e = take ? kNegInf : f;
           const float m = warp_max(e);
           const float s = warp_sum(exp2_fast((e - finite_ref(m)) * c));
@@ -859,26 +929,35 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       __syncwarp();
       bar_arrive(kSummed + turn, kSumThreads);
     }
+    if (flying) land();  // (after a wait that ran out)
   } else {
     // ------------------------------------------------ packets
     const int mine = warp - kWorkers - 1;
-    uint32_t* found = reinterpret_cast<uint32_t*>(hits + cap) + mine * (4 * cap + kBuckets);
-    int32_t* at = reinterpret_cast<int32_t*>(found + cap);  // keys, positions
-    uint32_t* order = found + 2 * cap;                      // keys, positions, buckets
-    int32_t* at2 = reinterpret_cast<int32_t*>(order + cap);
+    uint32_t* found =
+        reinterpret_cast<uint32_t*>(hits.bound + cap) + mine * (4 * room + kBuckets);
+    int32_t* at = reinterpret_cast<int32_t*>(found + room);  // keys, positions
+    uint32_t* order = found + 2 * room;                      // keys, positions, buckets
+    int32_t* at2 = reinterpret_cast<int32_t*>(order + room);
     int64_t number = mine;  // of the row among the CTA's
     for (int64_t row = blockIdx.x + mine * step; row < rows; row += PACK * step, number += PACK) {
       const int turn = (int)(number & 1);
       bar_sync(kSummed + turn, kSumThreads);
       const int slots = count;
-      const int n = slots <= cap ? warp_candidates<T>(hits, slots, found, at, cap) : cap + 1;
+      const float t = part_t[turn];
+      float dropped = kNegInf, dropped_s = 0.0f;
+      int n = room + 1;
+      if (slots <= cap)
+        n = chunks > 1 ? warp_candidates<T, true>(hits, slots, t, found, at, room, dropped)
+                       : warp_candidates<T, false>(hits, slots, t, found, at, room, dropped);
       const float mw = lane <= kWorkers ? part_m[turn][lane] : kNegInf;
       const float sw = lane <= kWorkers ? part_s[turn][lane] : 0.0f;
+      const float m = fmaxf(warp_max(mw), dropped), ref = finite_ref(m);
+      if (dropped != kNegInf) dropped_s = warp_dropped<T>(hits, slots, t, ref, c);
       __syncwarp();
       if (lane == 0) count = 0;
       __syncwarp();
       if (row + step < rows) bar_arrive(kListFree, 64);
-      if (n > cap) {
+      if (n > room) {
         if (lane == 0) {
           a.counts[row] = -1;
           again = 1;
@@ -886,11 +965,11 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         __syncwarp();
         continue;
       }
-      const float m = warp_max(mw), ref = finite_ref(m);
-      const float s = warp_sum(mw == kNegInf ? sw : sw * exp2_fast((mw - ref) * c));
-      if (n <= 128) warp_emit_few<4>(a, row, n, found, at, order + 2 * cap, at2, m, s);
-      else if (n <= 512) warp_emit_few<16>(a, row, n, found, at, order + 2 * cap, at2, m, s);
-      else warp_emit(a, row, n, found, at, order, at2, order + 2 * cap, m, s);
+      const float s =
+          warp_sum(mw == kNegInf ? sw : sw * exp2_fast((mw - ref) * c)) + dropped_s;
+      if (n <= 128) warp_emit_few<4>(a, row, n, found, at, order + 2 * room, at2, m, s);
+      else if (n <= 512) warp_emit_few<16>(a, row, n, found, at, order + 2 * room, at2, m, s);
+      else warp_emit(a, row, n, found, at, order, at2, order + 2 * room, m, s);
       __syncwarp();
     }
   }
@@ -911,9 +990,44 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
 // ---------------------------------------------------------------------------
 
 constexpr int kShortWarps = 4;  // per CTA
+// Up to this k the 32 lanes' maxima bound it well (12 of 32: some 15 candidates),
+// and each step of the search is one comparison instead of one per slot.
+constexpr int kLaneGroups = 12;
 
 __host__ __device__ constexpr size_t short_smem(int slots, int cap) {
   return (size_t)slots * 16 + (size_t)cap * 8;
+}
+
+// The packet of at most 32 candidates in ascending order of position, one per
+// lane: a candidate's rank is counted against all others.
+__device__ __forceinline__ void warp_emit_ranked(const TopkArgs& a, int64_t row, int n,
+                                                 const uint32_t* key, const int32_t* idx, float m,
+                                                 float s) {
+  const int lane = (int)lane_id(), k = a.k;
+  const uint32_t q = lane < n ? key[lane] : 0u;
+  int rank = lane < n ? 0 : 32;
+  for (int j = 0; j < n; ++j) {
+    const uint32_t other = __shfl_sync(kFull, q, j);
+    rank += other > q || (other == q && j < lane) ? 1 : 0;
+  }
+  const bool take = lane < n && rank < k;
+  const unsigned who = __ballot_sync(kFull, take);
+  const float x = lane < n && !take ? key_value(q) : kNegInf;
+  if (take) {
+    const int to = __popc(who & lanemask_lt());
+    a.values[row * k + to] = key_value(q);
+    a.indices[row * k + to] = idx[lane];
+  }
+  for (int j = min(k, n) + lane; j < k; j += 32) {
+    a.values[row * k + j] = 0.0f;
+    a.indices[row * k + j] = -1;
+  }
+  if (lane == 0) a.counts[row] = min(k, n);
+  if (a.tail == nullptr) return;
+  const float ref = finite_ref(fmaxf(warp_max(x), m));
+  float s2 = warp_sum(exp2_fast((x - ref) * a.c));
+  s2 += m != kNegInf ? s * exp2_fast((m - ref) * a.c) : s;  // (s is 0, or NaN)
+  if (lane == 0) a.tail[row] = s2 == 0.0f ? kNegInf : fmaf(ref, a.inv_tau, log2_fast(s2) * kLn2);
 }
 
 // The packet of n candidates in ascending order of position.
@@ -1046,21 +1160,30 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
     __syncwarp();
     uint4 raw[NV];
     uint32_t top[NV];
+    float most = kNegInf;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      raw[v] = v * 32 + lane < sh.slots ? buf[v * 32 + lane] : S::none();
-      top[v] = order_key(M::value(M::slot(raw[v])));
+      raw[v] = buf[v * 32 + lane];
+      if ((v + 1) * 32 > sh.slots && v * 32 + lane >= sh.slots) raw[v] = S::none();
+      const float x = M::value(M::slot(raw[v]));
+      most = NanMax<float>::of(most, x);
+      top[v] = group_key(x);
     }
     __syncwarp();
     if (row + step < rows) fetch(row + step);
     uint32_t bound = 0;
-    if (k > 0)
+    if (k > 0 && k <= kLaneGroups) {
+      // a lane is a group: one key per lane
+      const uint32_t own = group_key(most);
+      bound = warp_bound([&](auto f) { f(own); }, k, k + k / 4 + 2);
+    } else if (k > 0) {
       bound = warp_bound(
           [&](auto f) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) f(top[v]);
           },
           k, k + k / 4 + 4);
+    }
     const float t = bound_value<T>(bound, k);
     const Above<T> above(t);
 
@@ -1093,20 +1216,36 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
 #pragma unroll
         for (int e = 0; e < N; ++e)
           bits |= !((e & 1 ? f[e / 2].y : f[e / 2].x) < t) ? 1u << e : 0u;
-        const uint32_t mine = __popc(bits);
-        const uint32_t before = __any_sync(kFull, mine > 1) ? warp_incl_scan(mine) - mine
-                                                            : __popc(who & lanemask_lt());
-        int to = n + (int)before;
+        const int at = sh.head + (v * 32 + lane) * N;
+        if (!__any_sync(kFull, (bits & (bits - 1)) != 0)) {  // one each
+          const int to = n + __popc(who & lanemask_lt());
+          if (some && to < cap) {
+            const int i = __ffs(bits) - 1;
+            float x = f[0].x;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (bits >> e & 1u) {
-            if (to < cap) {
-              key[to] = order_key(e & 1 ? f[e / 2].y : f[e / 2].x);
-              idx[to] = sh.head + (v * 32 + lane) * N + e;
-            }
-            ++to;
+            for (int e = 1; e < N; ++e)
+              if (e == i) x = e & 1 ? f[e / 2].y : f[e / 2].x;
+            key[to] = order_key(x);
+            idx[to] = at + i;
           }
-        n += (int)__reduce_add_sync(kFull, mine);
+          n += __popc(who);
+        } else {
+          const uint32_t mine = __popc(bits);
+          int to = n + (int)(warp_incl_scan(mine) - mine);
+#pragma unroll 1
+          for (uint32_t left = bits; left != 0; left &= left - 1, ++to) {
+            const int i = __ffs(left) - 1;
+            float x = f[0].x;
+#pragma unroll
+            for (int e = 1; e < N; ++e)
+              if (e == i) x = e & 1 ? f[e / 2].y : f[e / 2].x;
+            if (to < cap) {
+              key[to] = order_key(x);
+              idx[to] = at + i;
+            }
+          }
+          n += (int)__reduce_add_sync(kFull, mine);
+        }
       }
     }
     append(edge_in && !at_head, edge, S::edge_at(sh, lane));
@@ -1133,7 +1272,8 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
         again = 1;
       }
     } else {
-      warp_emit_sorted(a, row, n, key, idx, m, s);
+      if (n <= 32) warp_emit_ranked(a, row, n, key, idx, m, s);
+      else warp_emit_sorted(a, row, n, key, idx, m, s);
     }
     __syncwarp();
   }
@@ -1156,34 +1296,52 @@ int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
   return (int64_t)sms * fit < most ? (int64_t)sms * fit : most;
 }
 
+// How a form cuts rows of a vocabulary, and the shared memory it takes.
+struct StreamPlan {
+  int chunks, per, cap, room;
+  size_t smem;
+};
 template <typename T, int WARPS, int PACK, int NV, int GPT>
-void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
+StreamPlan plan_stream(const TopkArgs& a) {
   using Sh = TopkShape<WARPS, PACK, NV, GPT>;
-  const auto kernel = topk_stream<T, WARPS, PACK, NV, GPT>;
+  StreamPlan p;
   const int64_t slots = a.vocab / Slot<T>::N + 1;
-  const int chunks = (int)((slots + Sh::kCap - 1) / Sh::kCap);
-  const int per = (int)((slots + chunks - 1) / chunks);
+  p.chunks = (int)((slots + Sh::kCap - 1) / Sh::kCap);
+  p.per = (int)((slots + p.chunks - 1) / p.chunks);
   // candidates: c groups of G at or above the bound mean -G ln(1 - c / G) of a
-  // first chunk's elements, and a 1 / i-th of that in the i-th
+  // first chunk's elements, as many of the second's, which is held against the
+  // first's bound, half as many of the third's, and so on; of all those the
+  // first number lies above the last bound
   const int64_t groups = slots < Sh::kGroups ? slots : Sh::kGroups;
   const double c = 1.125 * a.k + 4;
-  int64_t cap = a.vocab;
+  int64_t cap = a.vocab, room = a.vocab;
   if (c < 0.8 * (double)groups) {
-    double chunk_sum = 0.0;
-    for (int i = 1; i <= chunks && i <= 64; ++i) chunk_sum += 1.0 / i;
-    cap = (int64_t)(-(double)groups * std::log(1.0 - c / (double)groups) * chunk_sum * 1.15) + 96;
+    double chunk_sum = 1.0;
+    for (int i = 1; i < p.chunks && i <= 64; ++i) chunk_sum += 1.0 / i;
+    const double one = -(double)groups * std::log(1.0 - c / (double)groups) * 1.15;
+    cap = (int64_t)(one * chunk_sum) + 96;
+    room = (int64_t)one + 96;
   }
-  if (cap > a.vocab) cap = a.vocab;
-  const int64_t room = (216 * 1024 - (int64_t)topk_smem(Sh::kCap, Sh::kGroups, 0, PACK)) /
-                       (int64_t)(sizeof(Hit) + 16 * PACK);
-  if (cap > room) cap = room;
-  cap = (cap + 3) & ~3;
-  const size_t smem = topk_smem(Sh::kCap, Sh::kGroups, (int)cap, PACK);
-  if (smem > 48 * 1024)
-    (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  const int64_t grid = resident(sms, 32 / WARPS, smem, rows);
-  launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), smem, s, a, rows, chunks, per,
-             (int)cap);
+  const auto within = [](int64_t x, int64_t y, int64_t most) {
+    const int64_t n = x < y ? x : y;
+    return ((int)(n < most ? n : most) + 3) & ~3;
+  };
+  const int64_t left = 214 * 1024 - (int64_t)topk_smem(Sh::kCap, Sh::kGroups, 0, 0, PACK);
+  p.cap = within(cap, a.vocab, left / 2 / kHitBytes);
+  p.room = within(room, a.vocab, left / 2 / (16 * PACK));
+  p.smem = topk_smem(Sh::kCap, Sh::kGroups, p.cap, p.room, PACK);
+  return p;
+}
+
+template <typename T, int WARPS, int PACK, int NV, int GPT>
+void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
+  const auto kernel = topk_stream<T, WARPS, PACK, NV, GPT>;
+  const StreamPlan p = plan_stream<T, WARPS, PACK, NV, GPT>(a);
+  if (p.smem > 48 * 1024)
+    (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  const int64_t grid = resident(sms, 32 / WARPS, p.smem, rows);
+  launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), p.smem, s, a, rows, p.chunks, p.per,
+             p.cap, p.room);
 }
 
 template <typename T, int NV>
@@ -1213,7 +1371,14 @@ void launch_typed(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   else if (slots <= TopkShape<4, 1, 8, 8>::kCap && a.k <= 128)
     launch_stream<T, 4, 1, 8, 8>(a, rows, sms, s);
   else if (slots <= TopkShape<8, 1, 8, 8>::kCap) launch_stream<T, 8, 1, 8, 8>(a, rows, sms, s);
-  else if (a.k <= 256) launch_stream<T, 16, 2, 10, 1>(a, rows, sms, s);
+  else if (a.k <= 256) {
+    // two CTAs per SM where there are rows for them, if need be with less room
+    // (1024 rows of 131071 fp16 logits, k 256: 150 us, else 199)
+    if (rows > sms && resident(1, 2, plan_stream<T, 16, 2, 10, 1>(a).smem, 2) < 2)
+      launch_stream<T, 16, 1, 8, 2>(a, rows, sms, s);
+    else
+      launch_stream<T, 16, 2, 10, 1>(a, rows, sms, s);
+  }
   else launch_stream<T, 16, 2, 10, 10>(a, rows, sms, s);
 }
 
