@@ -583,13 +583,25 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     if (nx.rank == 0 && lane < nx.shape.edge) nx.end = x[S::edge_at(nx.shape, lane)];
     return nx;
   };
-  bool lost = false;  // a wait ran out: every row from there on is NaN
+  bool lost = false;    // a wait ran out: every row from there on is NaN
+  bool flying = false;  // a copy is under way
+  uint32_t phase = 0;
   const auto start_copy = [&](const Next& nx) {
-    if (lane == 0 && !lost) {
+    if (lost) return;
+    flying = true;
+    if (lane == 0) {
       const T* x = static_cast<const T*>(a.logits) + nx.row * a.stride + nx.shape.head;
       mbar_expect(&full, (uint32_t)nx.held * 16);
       if (nx.held > 0)
         bulk_copy(buf, reinterpret_cast<const uint4*>(x) + nx.lo, (uint32_t)nx.held * 16, &full);
+    }
+  };
+  const auto land = [&] {  // waits for the copy under way
+    if (flying && __all_sync(kFull, mbar_wait(&full, phase))) {
+      flying = false;
+      phase ^= 1;
+    } else {
+      lost = true;
     }
   };
   const auto packet_at = [&](int turn) { return words + turn * 4 * kpad; };
@@ -601,7 +613,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     }
   };
 
-  uint32_t phase = 0, peer_phase = 0;
+  uint32_t peer_phase = 0;
   int turn = 0, side = 0;
   // row being prepared
   Part on;
@@ -618,9 +630,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     w = GRAD ? me.row_grad * a.inv_tau : 0.0f;
     end = me.rank == 0 && lane < me.shape.edge ? to_f32(me.end) : kNegInf;
     copy_async_wait();
-    if (!lost && !mbar_wait(&full, phase)) lost = true;
-    phase ^= 1;
-    lost = __any_sync(kFull, lost);
+    land();
     bad = lost;
     on = no_part();
     if (LOSS && lane == 0 && me.held < per) buf[me.held] = S::none();
@@ -680,6 +690,50 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         if (sx[j] != kNegInf) g[idx[j]] = from_f32<T>(grad_on(r, c, sx[j], tx[j]));
   };
 
+  const float nan = __int_as_float(0x7FFFFFFF);
+  // joins the warps' sums (one pair per lane) with the packet's, and the
+  // cluster's, and writes the row's loss
+  const auto conclude = [&](const Next& me, Part all, float mw, float sw, bool bad, float w) {
+    all.m_off = warp_max(mw);
+    all.s_off = warp_sum(sw * rescale(mw, all.m_off, c));
+    if (cluster > 1 && !bad) {
+      if (lane < cluster) {
+        *cg::this_cluster().map_shared_rank(&peers[side][cl_rank], lane) = all;
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_addr(&peer)), "r"(lane));
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at)
+                     : "memory");
+      }
+      __syncwarp();
+      if (!mbar_wait(&peer, peer_phase)) lost = true;
+      lost = __any_sync(kFull, lost);
+      peer_phase ^= 1;
+      all = join(lane < cluster ? peers[side][lane] : no_part(), cluster, c);
+#pragma unroll
+      for (int q = 0; q < (int)(sizeof(Part) / 4); ++q) {
+        float* v = reinterpret_cast<float*>(&all) + q;
+        *v = __shfl_sync(kFull, *v, 0);
+      }
+      side ^= 1;
+      bad = lost;
+    }
+    const bool write = me.rank == 0 && lane == 0;
+    Row r = finish_row(all, a, w, me.tail, write ? a.loss + me.row : nullptr,
+                       write && a.stats ? a.stats + me.row * 6 : nullptr);
+    if (bad) {
+      r.coef = r.poison = nan;
+      r.dead = w == 0.0f;
+      if (write) {
+        a.loss[me.row] = nan;
+        if (a.stats)
+          for (int q = 0; q < 6; ++q) a.stats[me.row * 6 + q] = nan;
+      }
+    }
+    return r;
+  };
+
   if (first >= items) {
     if (cluster > 1) cg::this_cluster().sync();
     return;
@@ -688,23 +742,31 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   start_copy(me);
   start_packet(me, 0);
   prepare(me, 0);
-  Row r;
-  Next last;        // the row before, whose gradient is not finished
+  // the row before: its gradient (GRAD), or all of its end (loss alone: nobody
+  // waits for it, so it is concluded while the others read the next row)
+  Next last;
   Row last_r;
+  Part last_on;
+  float last_m = kNegInf, last_s = 0.0f, last_end = 0.0f;
   int last_n = 0;
-  float last_end = 0.0f;
-  const float nan = __int_as_float(0x7FFFFFFF);
+  bool last_bad = false;
   for (int64_t item = first; item < items; item += step, turn ^= 1) {
     if (!LOSS) {
-      r = stored_row(a, me.row, w);
+      Row r = stored_row(a, me.row, w);
       if (bad) r.coef = nan;
       r.dead = w == 0.0f || (r.dead && !bad);
       if (lane == 0) row_sh[turn] = r;
+      __syncwarp();
+      if (item != first) bar_sync(kStored, kThreads);
+      bar_sync(kReady, kThreads);
+      if (item != first) finish_grad(last, turn ^ 1, last_r, last_n, last_end);
+      last_r = r;
+    } else {
+      __syncwarp();
+      if (GRAD && item != first) bar_sync(kStored, kThreads);
+      bar_sync(kReady, kThreads);
+      if (GRAD && item != first) finish_grad(last, turn ^ 1, last_r, last_n, last_end);
     }
-    __syncwarp();
-    if (GRAD && item != first) bar_sync(kStored, kThreads);
-    bar_sync(kReady, kThreads);
-    if (GRAD && item != first) finish_grad(last, turn ^ 1, last_r, last_n, last_end);
     __syncwarp();
     const bool more = item + step < items;
     Next nx;
@@ -741,53 +803,17 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       const float m_end = warp_max(end);
       const float s_end = warp_sum(exp2_fast((end - finite_ref(m_end)) * c));
       bar_sync(kParts, kThreads);
-      const float mw = lane < kWorkers ? part_m[lane] : lane == kWorkers ? m_end : kNegInf;
-      const float sw = lane < kWorkers ? part_s[lane] : lane == kWorkers ? s_end : 0.0f;
-      on.m_off = warp_max(mw);
-      on.s_off = warp_sum(sw * rescale(mw, on.m_off, c));
-      if (cluster > 1 && !bad) {
-        if (lane < cluster) {
-          *cg::this_cluster().map_shared_rank(&peers[side][cl_rank], lane) = on;
-          uint32_t at;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                       : "=r"(at)
-                       : "r"(smem_addr(&peer)), "r"(lane));
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at)
-                       : "memory");
-        }
-        __syncwarp();
-        if (!mbar_wait(&peer, peer_phase)) lost = true;
-        lost = __any_sync(kFull, lost);
-        peer_phase ^= 1;
-        on = join(lane < cluster ? peers[side][lane] : no_part(), cluster, c);
-#pragma unroll
-        for (int q = 0; q < (int)(sizeof(Part) / 4); ++q) {
-          float* v = reinterpret_cast<float*>(&on) + q;
-          *v = __shfl_sync(kFull, *v, 0);
-        }
-        side ^= 1;
-        bad = lost;
-      }
-      const bool write = me.rank == 0 && lane == 0;
-      r = finish_row(on, a, w, me.tail, write ? a.loss + me.row : nullptr,
-                     write && a.stats ? a.stats + me.row * 6 : nullptr);
-      if (bad) {
-        r.coef = r.poison = nan;
-        r.dead = w == 0.0f;
-        if (write) {
-          a.loss[me.row] = nan;
-          if (a.stats)
-            for (int q = 0; q < 6; ++q) a.stats[me.row * 6 + q] = nan;
-        }
-      }
+      last_m = lane < kWorkers ? part_m[lane] : lane == kWorkers ? m_end : kNegInf;
+      last_s = lane < kWorkers ? part_s[lane] : lane == kWorkers ? s_end : 0.0f;
+      last_r = conclude(me, on, last_m, last_s, bad, w);
+      bad |= lost;
       if (GRAD) {
-        if (lane == 0) row_sh[turn] = r;
+        if (lane == 0) row_sh[turn] = last_r;
         __syncwarp();
         bar_sync(kRowDone, kThreads);
       }
     }
     last = me;
-    last_r = r;
     last_n = bad ? 0 : n;
     last_end = end;
     if (more) {
@@ -800,7 +826,314 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
     bar_sync(kStored, kThreads);
     finish_grad(last, turn ^ 1, last_r, last_n, last_end);
   }
+  if (flying) land();  // (after a wait that ran out)
   if (cluster > 1) cg::this_cluster().sync();
+}
+
+// ---------------------------------------------------------------------------
+// Losses alone, of rows enough to fill the device with a CTA each: nothing of a
+// row is needed again, so no CTA has to hold one.  A persistent grid; a CTA
+// takes its rows in chunks through a ring of buffers, four CTAs per SM.  The row
+// warp keeps the ring filled, takes the packet's logits out of each chunk before
+// the others may read it, and concludes a row while the others read the next;
+// the others keep one running maximum and sum per thread and meet once per row.
+// ---------------------------------------------------------------------------
+
+constexpr int kRingWarps = 8, kRingStages = 3, kRingNV = 4;
+constexpr int kRingWorkers = kRingWarps - 1;
+constexpr int kRingChunk = kRingWorkers * 32 * kRingNV;  // slots
+
+// Shared memory in bytes: the ring, two packets (indices, values) and the
+// current one's logits on both sides.
+__host__ __device__ constexpr size_t ring_smem(int kpad) {
+  return (size_t)kRingStages * kRingChunk * 16 + (size_t)kpad * 24;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRingWarps * 32, 4)
+    distill_ring(DistillArgs a, int64_t rows, int kpad) {
+  using S = Slot<T>;
+  constexpr int N = S::N;
+  constexpr int kLanes = kRingWorkers * 32;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part_m[2][kRingWorkers], part_s[2][kRingWorkers];
+  struct Info {
+    int held, last;
+  };
+  __shared__ Info info_sh[kRingStages];
+  // a chunk is there; may be read; has been read; a row's sums are there
+  __shared__ __align__(8) uint64_t full[kRingStages], ready[kRingStages], empty[kRingStages];
+  __shared__ __align__(8) uint64_t summed[2];
+  uint4* ring = reinterpret_cast<uint4*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = a.c;
+  const int64_t step = gridDim.x;
+
+  if (tid == 0) {
+    for (int q = 0; q < kRingStages; ++q) {
+      mbar_init(&full[q], 1);
+      mbar_init(&ready[q], 1);
+      mbar_init(&empty[q], kRingWorkers);
+    }
+    mbar_init(&summed[0], kRingWorkers);
+    mbar_init(&summed[1], kRingWorkers);
+    fence_bulk();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // a place in the ring and the parity of its current use
+  struct Place {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+      if (++at == kRingStages) {
+        at = 0;
+        parity ^= 1;
+      }
+    }
+  };
+
+  if (warp < kRingWorkers) {
+    Place p;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
+      float m = kNegInf;
+      float2 sum = make_float2(0.0f, 0.0f);
+      for (bool last = false; !last; p.next()) {
+        // (a wait that ran out: the row warp's do as well, and the rows are NaN)
+        if (!__all_sync(kFull, mbar_wait(&ready[p.at], p.parity))) return;
+        const Info info = info_sh[p.at];
+        const uint4* buf = ring + p.at * kRingChunk;
+        last = info.last != 0;
+        uint4 raw[kRingNV];
+        SlotMax<T> slot_max;
+#pragma unroll
+        for (int v = 0; v < kRingNV; ++v) {
+          const int q = v * kLanes + tid;
+          raw[v] = q < info.held ? buf[q] : S::none();
+          slot_max.add(raw[v]);
+          forget(raw[v]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[p.at]);
+        const float top = fmaxf(m, slot_max.get()), ref = finite_ref(top);
+        const float scale = rescale(m, top, c);
+        sum = mul2(sum, make_float2(scale, scale));
+        m = top;
+#pragma unroll
+        for (int v = 0; v < kRingNV; ++v) {
+          float2 f[N / 2];
+          exp2_slot<T>(raw[v], ref, c, 0.0f, f);
+          sum_slot<T>(f, sum);
+          forget(raw[v]);
+        }
+      }
+      const float most = warp_max(m);
+      const float s = warp_sum((sum.x + sum.y) * (m == kNegInf ? 1.0f : rescale(m, most, c)));
+      if (lane == 0) {
+        part_m[turn][warp] = most;
+        part_s[turn][warp] = s;
+        mbar_arrive(&summed[turn]);
+      }
+    }
+    return;
+  }
+
+  // ------------------------------------------------------------------ row warp
+  const int vocab = a.vocab;
+  const float nan = __int_as_float(0x7FFFFFFF);
+  bool lost = false;  // a wait ran out: every row from there on is NaN
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!lost) lost = !__all_sync(kFull, mbar_wait(bar, parity));
+  };
+  // the chunks in order; one cursor for the copies, one for the work
+  struct Cursor {
+    int64_t row;
+    RowShape shape;
+    int per, chunks, ch;
+    __device__ __forceinline__ int lo() const { return ch * per; }
+    __device__ __forceinline__ int held() const { return min(per, shape.slots - ch * per); }
+  };
+  const auto enter = [&](int64_t row) {
+    Cursor q;
+    q.row = row;
+    q.shape = S::shape(static_cast<const T*>(a.logits) + row * a.stride, vocab);
+    q.chunks = (q.shape.slots + kRingChunk - 1) / kRingChunk;
+    q.per = (q.shape.slots + q.chunks - 1) / q.chunks;
+    q.ch = 0;
+    return q;
+  };
+  Cursor ahead = enter(blockIdx.x);
+  Place into;      // the next copy's
+  int flying = 0;  // copies under way
+  const auto start_copy = [&] {
+    if (ahead.row >= rows || lost) return;
+    if (lane == 0) {
+      const T* x = static_cast<const T*>(a.logits) + ahead.row * a.stride + ahead.shape.head;
+      mbar_expect(&full[into.at], (uint32_t)ahead.held() * 16);
+      bulk_copy(ring + into.at * kRingChunk, reinterpret_cast<const uint4*>(x) + ahead.lo(),
+                (uint32_t)ahead.held() * 16, &full[into.at]);
+    }
+    __syncwarp();
+    ++flying;
+    into.next();
+    if (++ahead.ch == ahead.chunks) ahead = enter(ahead.row + step);
+  };
+  float* words = reinterpret_cast<float*>(smem + (size_t)kRingStages * kRingChunk * 16);
+  float *sx = words + 4 * kpad, *tx = words + 5 * kpad;
+  // what is known of a row before it is worked on
+  struct Next {
+    int count;  // as loaded, like the following: a conversion would wait
+    float tail;
+    T end;
+  } nx;
+  const auto describe = [&](int64_t row, int turn) {
+    const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+    const RowShape shape = S::shape(x, vocab);
+    nx.count = a.counts ? a.counts[row] : a.k;
+    nx.tail = a.tail ? a.tail[row] : 0.0f;
+    if (lane < shape.edge) nx.end = x[S::edge_at(shape, lane)];
+    float* p = words + turn * 2 * kpad;
+    for (int j = lane; j < a.k; j += 32) {
+      copy_async4(p + j, a.indices + row * a.k + j);
+      copy_async4(p + kpad + j, a.values + row * a.k + j);
+    }
+  };
+
+#pragma unroll 1
+  for (int q = 0; q < kRingStages; ++q) start_copy();
+  describe(blockIdx.x, 0);
+  // the row before, which is still to be concluded
+  Part last;
+  float last_tail = 0.0f, end_m = kNegInf, end_s = 0.0f;
+  bool last_bad = false;
+  int64_t open = blockIdx.x;  // the first row that is not concluded
+  uint32_t sum_parity = 0;
+  const auto conclude = [&](int turn) {
+    wait(&summed[turn], sum_parity);
+    sum_parity ^= (uint32_t)turn;
+    const float mw = lane < kRingWorkers ? part_m[turn][lane] : lane == kRingWorkers ? end_m : kNegInf;
+    const float sw = lane < kRingWorkers ? part_s[turn][lane] : lane == kRingWorkers ? end_s : 0.0f;
+    last.m_off = warp_max(mw);
+    last.s_off = warp_sum(mw == kNegInf ? sw : sw * rescale(mw, last.m_off, c));
+    const bool bad = last_bad || lost;
+    finish_row(last, a, 0.0f, last_tail, lane == 0 && !bad ? a.loss + open : nullptr,
+               a.stats ? a.stats + open * 6 : nullptr);
+    if (bad && lane == 0) {
+      a.loss[open] = nan;
+      if (a.stats)
+        for (int q = 0; q < 6; ++q) a.stats[open * 6 + q] = nan;
+    }
+    open += step;
+  };
+
+  Place p;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += step, turn ^= 1) {
+    Cursor now = enter(row);
+    const int32_t* idx = reinterpret_cast<const int32_t*>(words + turn * 2 * kpad);
+    const float* val = words + (turn * 2 + 1) * kpad;
+    Part on = no_part();
+    copy_async_wait();
+    __syncwarp();
+    const int n = min(max(nx.count, 0), a.k);
+    const float tail = nx.tail;
+    float end = lane < now.shape.edge ? to_f32(nx.end) : kNegInf;
+    bool bad = false;
+    int done = 0;  // entries that were seen
+    for (; now.ch < now.chunks; ++now.ch, p.next()) {
+      const bool final = now.ch + 1 == now.chunks;
+      const int lo = now.lo(), held = now.held();
+      wait(&full[p.at], p.parity);
+      if (lost) break;
+      --flying;
+      T* buf = reinterpret_cast<T*>(ring + p.at * kRingChunk);
+      // the entries before the chunk's end, in the last chunk all the others
+      const int limit = final ? 0x7FFFFFFF : now.shape.head + (lo + held) * N;
+      for (int some = 32; some == 32;) {
+        const int j = done + lane;
+        const int i = j < n ? idx[j] : 0x7FFFFFFF;
+        const unsigned in = __ballot_sync(kFull, j < n && (i < limit || final));
+        some = in == kFull ? 32 : __ffs(~in) - 1;
+        const bool mine = lane < some;
+        int e = -1;  // the entry's place among the row's ends
+        float s = kNegInf;
+        if (mine) {
+          const int before = j > 0 ? idx[j - 1] : -1;
+          const int pos = i - now.shape.head, q = pos - lo * N;
+          if (i <= before || i < 0 || i >= vocab) {
+            bad = true;
+          } else if (pos < 0 || pos >= now.shape.slots * N) {
+            e = pos < 0 ? i : i - now.shape.slots * N;
+          } else if (q >= 0 && q < held * N) {
+            s = to_f32(buf[q]);
+            buf[q] = from_f32<T>(kNegInf);
+          }
+        }
+        if (__any_sync(kFull, e >= 0)) {
+          const float at_end = __shfl_sync(kFull, end, e & 31);
+          if (e >= 0) s = at_end;
+          const unsigned gone = __reduce_or_sync(kFull, e >= 0 ? 1u << e : 0u);
+          if (gone >> lane & 1u) end = kNegInf;
+        }
+        if (mine) {
+          const float t = s == kNegInf ? kNegInf : val[j];
+          sx[j] = s;
+          tx[j] = t;
+          on.m_s = fmaxf(on.m_s, s);
+          on.m_t = fmaxf(on.m_t, t);
+        }
+        done += some;
+      }
+      if (lane == 0) info_sh[p.at] = Info{held, final};
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[p.at]);
+      if (now.ch == 0) {
+        if (row + step < rows) describe(row + step, turn ^ 1);
+        if (open != row) conclude(turn ^ 1);
+      }
+      // the chunk before this one has been read: its buffer is free again
+      if (now.ch > 0 || row != (int64_t)blockIdx.x) {
+        const int was = p.at == 0 ? kRingStages - 1 : p.at - 1;
+        wait(&empty[was], p.at == 0 ? p.parity ^ 1 : p.parity);
+        fence_bulk();
+        __syncwarp();
+        start_copy();
+      }
+    }
+    // the packet's sums and the row's ends
+    on.m_s = warp_max(on.m_s);
+    on.m_t = warp_max(on.m_t);
+    const float rs = finite_ref(on.m_s), rt = finite_ref(on.m_t);
+    if (lost) break;
+    __syncwarp();
+    for (int j = lane; j < n; j += 32) {
+      const float y = tx[j] - rt, z = sx[j] - rs;
+      const float e = exp2_fast(y * c);
+      on.s_s += exp2_fast(z * c);
+      on.s_t += e;
+      if (e != 0.0f) on.u += e * kUnit * (y - z);
+    }
+    on.s_s = warp_sum(on.s_s);
+    on.s_t = warp_sum(on.s_t);
+    on.u = warp_sum(on.u);
+    end_m = warp_max(end);
+    end_s = warp_sum(exp2_fast((end - finite_ref(end_m)) * c));
+    last = on;
+    last_tail = tail;
+    last_bad = __any_sync(kFull, bad);
+    __syncwarp();
+  }
+  if (!lost) conclude(turn ^ 1);
+  // after a wait that ran out: what is not concluded is NaN, copies are let land
+  for (; open < rows; open += step)
+    if (lane == 0) {
+      a.loss[open] = nan;
+      if (a.stats)
+        for (int q = 0; q < 6; ++q) a.stats[open * 6 + q] = nan;
+    }
+  for (; flying > 0; --flying, p.next()) mbar_wait(&full[p.at], p.parity);
 }
 
 // ---------------------------------------------------------------------------
@@ -1083,6 +1416,16 @@ void launch_stream(const DistillArgs& a, int64_t rows, int per, int cluster, int
                        s, a, per, cluster, shares, items, kpad);
 }
 
+template <typename T>
+void launch_ring(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
+  const auto kernel = distill_ring<T>;
+  const int kpad = (a.k + 3) & ~3;
+  const size_t smem = ring_smem(kpad);
+  const int64_t grid = resident(sms, 4, smem, rows);
+  (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  launch_pdl(kernel, dim3((unsigned)grid), dim3(kRingWarps * 32), smem, s, a, rows, kpad);
+}
+
 template <typename T, int NV, bool LOSS, bool GRAD>
 void launch_short(const DistillArgs& a, int64_t rows, int per, int shares, int sms,
                   cudaStream_t s) {
@@ -1103,6 +1446,15 @@ template <typename T, bool LOSS, bool GRAD>
 void launch_typed(const DistillArgs& a, int64_t rows, int sms, cudaStream_t s) {
   const int64_t slots = a.vocab / Slot<T>::N + 1;
   constexpr int kMost = held_by(16, 9);
+  // losses alone of rows that one CTA cannot hold: a CTA per row, chunk by
+  // chunk, once there are two rows per SM (2288 rows of 131071 bf16 logits: 109
+  // us, as clusters 153; 160 such rows: 21, as clusters 15; rows that one CTA
+  // holds, 9828 of 30522: 133, held 94)
+  if constexpr (LOSS && !GRAD)
+    if (slots > kMost && rows >= 2 * sms) {
+      launch_ring<T>(a, rows, sms, s);
+      return;
+    }
   int cluster = 1, shares = 1;
   if (LOSS) {
     // a row on one CTA while it fits its registers and there are rows enough

@@ -135,6 +135,9 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 // Waits for the phase of the given parity, at most kWaitLimitNs; false if it
 // ran out.  (The wait itself suspends the thread for a while; the clock is
 // read only when it comes back empty-handed.)
