@@ -166,25 +166,26 @@ __device__ __noinline__ void plain_row(const TopkArgs& a, int64_t row, uint32_t*
 // ---------------------------------------------------------------------------
 
 // A key t with at least k of a warp's keys at or above it, and not many more:
-// the search stops at `most`.  Returns 0 if fewer than k keys are above -Inf.
-// `each(f)` calls f with every key of this lane.
+// the search stops at `most`.  `from` is one with at least k (0: none is known);
+// returns 0 if fewer than k keys are above -Inf.  `each(f)` calls f(key, q) with
+// every key of this lane, q-th of them.
 template <typename Each>
-__device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
+__device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most, uint32_t from = 0) {
   uint32_t hi = 0, lo = 0xFFFFFFFFu, any = 0, all = 0xFFFFFFFFu;
   int live = 0;
-  each([&](uint32_t q) {
-    hi = max(hi, q);
-    lo = min(lo, q);
-    any |= q;
-    all &= q;
-    live += q > kKeyNegInf ? 1 : 0;
+  each([&](uint32_t key, int) {
+    hi = max(hi, key);
+    lo = min(lo, key);
+    any |= key;
+    all &= key;
+    live += key > kKeyNegInf ? 1 : 0;
   });
   hi = __reduce_max_sync(kFull, hi);
   // bits below `end` are the same in every key (a narrow type's)
   const uint32_t vary = __reduce_or_sync(kFull, any) & ~__reduce_and_sync(kFull, all);
   const int end = __ffs(vary) - 1;
-  lo = max(__reduce_min_sync(kFull, lo), kKeyNegInf + 1);
-  if (__reduce_add_sync(kFull, live) < k) return 0;
+  lo = max(__reduce_min_sync(kFull, lo), max(kKeyNegInf + 1, from));
+  if (from == 0 && __reduce_add_sync(kFull, live) < k) return 0;
   // t keeps count(t) >= k
   uint32_t t = lo;
   const uint32_t differ = hi ^ lo;
@@ -193,12 +194,16 @@ __device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
     t = lo & ~((2u << top) - 1u);  // the common prefix: every key is at or above it
     for (int b = top; b >= end; --b) {
       const uint32_t mid = t | (1u << b);
-      int c = 0;
-      each([&](uint32_t q) { c += q >= mid ? 1 : 0; });
-      c = __reduce_add_sync(kFull, c);
-      if (c >= k) {
+      if (mid > hi) continue;
+      if (mid > lo) {
+        int c[4] = {0, 0, 0, 0};  // (four sums: no long chain of additions)
+        each([&](uint32_t key, int q) { c[q & 3] += key >= mid ? 1 : 0; });
+        const int n = __reduce_add_sync(kFull, c[0] + c[1] + c[2] + c[3]);
+        if (n < k) continue;
         t = mid;
-        if (c <= most) break;
+        if (n <= most) break;
+      } else {
+        t = mid;
       }
     }
     t = max(t, lo);
@@ -209,7 +214,8 @@ __device__ __forceinline__ uint32_t warp_bound(Each each, int k, int most) {
 // The bound over keys in shared memory, REGS of them per lane in registers; 0:
 // n of them (a multiple of 4), read four at a time for each step.
 template <int REGS>
-__device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int k) {
+__device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int k,
+                                               uint32_t from) {
   const int lane = (int)lane_id();
   const int most = k + k / 8 + 4;
   if constexpr (REGS > 0) {
@@ -219,33 +225,37 @@ __device__ __forceinline__ uint32_t keys_bound(const uint32_t* keys, int n, int 
     return warp_bound(
         [&](auto f) {
 #pragma unroll
-          for (int q = 0; q < REGS; ++q) f(own[q]);
+          for (int q = 0; q < REGS; ++q) f(own[q], q);
         },
-        k, most);
+        k, most, from);
   } else {
     const uint4* four = reinterpret_cast<const uint4*>(keys);
     return warp_bound(
         [&](auto f) {
           for (int i = lane; i < n / 4; i += 32) {
             const uint4 q = four[i];
-            f(q.x);
-            f(q.y);
-            f(q.z);
-            f(q.w);
+            f(q.x, 0);
+            f(q.y, 1);
+            f(q.z, 2);
+            f(q.w, 3);
           }
         },
-        k, most);
+        k, most, from);
   }
 }
 
 // The value a bound stands for, rounded to the logits' type: a value between
 // two of the type's rounds to the upper one (the same elements) or to the lower
-// one (more candidates than needed).  -Inf itself is never a candidate.
+// one (more candidates than needed).  -Inf itself is never a candidate, and a
+// NaN is no bound: where it is the k-th largest, NaN and +Inf are the candidates.
 template <typename T>
 __device__ __forceinline__ float bound_value(uint32_t key, int k) {
-  if (k == 0) return __int_as_float(0x7F800000);
+  const float inf = __int_as_float(0x7F800000);
+  if (k == 0) return inf;
+  if (key == 0) return Lowest<T>::value();
   const float t = to_f32(from_f32<T>(key_value(key)));
-  return key == 0 || t == kNegInf ? Lowest<T>::value() : t;
+  if (t != t) return inf;
+  return t == kNegInf ? Lowest<T>::value() : t;
 }
 
 constexpr int kBuckets = 512;
@@ -328,15 +338,12 @@ struct Hits {
 constexpr int kHitBytes = 24;
 
 // The candidates of n slots as keys and positions, in any order; returns their
-// number (more than there is room for: the rest is not there).  Elements below t, the last and
-// highest bound, are left out again (AGAIN: there may be such, as a row's bound
-// rises from chunk to chunk): `dropped` is the largest of them.
-template <typename T, bool AGAIN>
+// number (more than there is room for: the rest is not there).
+template <typename T>
 __device__ __forceinline__ int warp_candidates(const Hits& hits, int n, float t, uint32_t* key,
-                                               int32_t* idx, int room, float& dropped) {
+                                               int32_t* idx, int room) {
   constexpr int N = Slot<T>::N;
   int total = 0;
-  float most = kNegInf;
   for (int h0 = 0; h0 < n; h0 += 32) {
     const int h = h0 + (int)lane_id();
     const T* e = reinterpret_cast<const T*>(hits.raw + h);
@@ -344,16 +351,12 @@ __device__ __forceinline__ int warp_candidates(const Hits& hits, int n, float t,
     int at = 0;
     if (h < n) {
       const uint4 raw = hits.raw[h];
-      const float was = hits.bound[h];
       at = hits.at[h];
       float2 f[N / 2];
       Slot<T>::unpack(raw, f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
-        left |= !(x < t) ? 1u << i : 0u;
-        if (AGAIN && x < t && x >= was) most = fmaxf(most, x);
-      }
+      for (int i = 0; i < N; ++i)
+        left |= !((i & 1 ? f[i / 2].y : f[i / 2].x) < t) ? 1u << i : 0u;
     }
     for (unsigned who = __ballot_sync(kFull, left != 0); who != 0;
          who = __ballot_sync(kFull, left != 0)) {
@@ -369,11 +372,52 @@ __device__ __forceinline__ int warp_candidates(const Hits& hits, int n, float t,
     }
   }
   __syncwarp();
-  dropped = AGAIN ? warp_max(most) : kNegInf;
   return total;
 }
 
-// The sum of 2^((x - ref) c) over the elements that warp_candidates left out
+// The same for a row whose bound rose from chunk to chunk, to t: elements below
+// it that were held against less are left out again, `dropped` is the largest
+// of them.  There are many slots: four per lane at once.
+template <typename T>
+__device__ __forceinline__ int warp_candidates_again(const Hits& hits, int n, float t,
+                                                     uint32_t* key, int32_t* idx, int room,
+                                                     float& dropped) {
+  constexpr int N = Slot<T>::N, kAtOnce = 4;
+  const int lane = (int)lane_id();
+  int total = 0;
+  float most = kNegInf;
+  for (int h0 = 0; h0 < n; h0 += 32 * kAtOnce) {
+    uint32_t left = 0;  // N bits per slot
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      const int h = h0 + q * 32 + lane;
+      if (h >= n) continue;
+      const uint4 raw = hits.raw[h];
+      const float was = hits.bound[h];
+      float2 f[N / 2];
+      Slot<T>::unpack(raw, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
+        left |= !(x < t) ? 1u << (q * N + i) : 0u;
+        if (x < t && x >= was) most = fmaxf(most, x);
+      }
+    }
+    const uint32_t mine = __popc(left), end = warp_incl_scan(mine);
+    int to = total + (int)(end - mine);
+    total += (int)__shfl_sync(kFull, end, 31);
+    for (; left != 0 && to < room; left &= left - 1, ++to) {
+      const int i = __ffs(left) - 1, h = h0 + i / N * 32 + lane;
+      key[to] = order_key(to_f32(reinterpret_cast<const T*>(hits.raw + h)[i % N]));
+      idx[to] = hits.at[h] + i % N;
+    }
+    __syncwarp();
+  }
+  dropped = warp_max(most);
+  return total;
+}
+
+// The sum of 2^((x - ref) c) over the elements that were left out
 // again, none of them above ref.  As integers, so that the list's order does not
 // matter: 2^-31 of a term of 1 each.
 template <typename T>
@@ -693,6 +737,76 @@ __device__ __forceinline__ void warp_emit(const TopkArgs& a, int64_t row, int n,
 }
 
 // ---------------------------------------------------------------------------
+// A row once more, by the whole CTA, against a bound t that is known to be at
+// most its k-th largest element: where its chunks' lists overflowed because the
+// bound rose late (a row in ascending order, or many chunks of a large k).  One
+// pass; false if more than `room` elements reach t.  `work`: 4 room + kBuckets
+// words.
+// ---------------------------------------------------------------------------
+
+template <typename T>
+__device__ __noinline__ bool again_row(const TopkArgs& a, int64_t row, float t, uint32_t* work,
+                                       int room, int* count, float* red) {
+  using S = Slot<T>;
+  constexpr int N = S::N;
+  const T* x = static_cast<const T*>(a.logits) + row * a.stride;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const RowShape shape = S::shape(x, a.vocab);
+  uint32_t* key = work;
+  int32_t* idx = reinterpret_cast<int32_t*>(work + room);
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  float m = kNegInf, s = 0.0f;  // below t
+  const auto element = [&](float f, int at) {
+    if (f < t) return false;
+    const int to = atomicAdd(count, 1);
+    if (to < room) {
+      key[to] = order_key(f);
+      idx[to] = at;
+    }
+    return true;
+  };
+  if (tid < shape.edge) {
+    const int at = S::edge_at(shape, tid);
+    const float f = to_f32(x[at]);
+    if (!element(f, at) && f != kNegInf) {
+      m = f;
+      s = 1.0f;
+    }
+  }
+  const Above<T> above(t);
+  for (int q = tid; q < shape.slots; q += threads) {
+    uint4 raw = S::load(x, shape, q);
+    if (above.reached(NanMax<T>::slot(raw))) {
+      float2 f[N / 2];
+      S::unpack(raw, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        element(i & 1 ? f[i / 2].y : f[i / 2].x, shape.head + q * N + i);
+      above.take(raw);
+    }
+    SlotMax<T> below;
+    below.add(raw);
+    const float top = fmaxf(m, below.get()), ref = finite_ref(top);
+    if (m != kNegInf) s *= exp2_fast((m - ref) * a.c);
+    m = top;
+    float2 f[N / 2];
+    S::add(raw, -ref, f);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) s += exp2_fast(f[i].x * a.c) + exp2_fast(f[i].y * a.c);
+  }
+  const float top = block_max(m, red);
+  s = block_sum(m != kNegInf ? s * exp2_fast((m - finite_ref(top)) * a.c) : s, red);
+  __syncthreads();
+  const int n = *count;
+  if (n > room) return false;
+  if (tid < 32)
+    warp_emit(a, row, n, key, idx, work + 2 * room, idx + 2 * room, work + 4 * room, top, s);
+  __syncthreads();
+  return true;
+}
+
+// ---------------------------------------------------------------------------
 // A persistent grid; a CTA takes one row after another, in chunks that its
 // workers hold in registers.  The other warps: one has chunks copied to shared
 // memory ahead of time and finds the bound from the workers' maxima; PACK make
@@ -703,9 +817,13 @@ __device__ __forceinline__ void warp_emit(const TopkArgs& a, int64_t row, int n,
 // held against the bound of the chunks before them while the next one is
 // searched for, and what falls below the last bound is added to the tail by the
 // packet's warp.
-// 8192 rows of 30522 bf16 logits, k 64: 132 us, 3.8 TB/s; two CTAs per SM, each
-// waiting in turn for the bound's search (1.4 k cycles and more), its candidates
-// and the packet warps; the sums' exponentials are 10 us of it.
+// A row whose chunks hold more candidates than the lists (the bound rose late)
+// is read again, against its last bound.
+// 8192 rows of 30522 bf16 logits, k 64: 138 us, 3.6 TB/s; two CTAs per SM, each
+// waiting in turn for the bound's search (1.4 k cycles and more) and its
+// candidates; without the packets' warps it is 117 us, with a search of one step
+// 105, and the sums' exponentials are 10.  1024 rows of 131071 fp16 logits,
+// k 256: 117 us, without the packets 61.
 // GPT: groups per thread (its slots are dealt to them in runs).
 // ---------------------------------------------------------------------------
 
@@ -884,7 +1002,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       const bool has_edge = lane < shape.edge;
       const int edge_at = S::edge_at(shape, lane);
       const T edge = has_edge ? x[edge_at] : from_f32<T>(kNegInf);
-      float t = 0.0f;
+      uint32_t key = 0;  // the bound's
       for (int ch = 0; ch < chunks; ++ch) {
         land();
         // slots past the chunk: -Inf, where another chunk or row had elements
@@ -899,11 +1017,14 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
         if (more) now = ch + 1 < chunks ? piece(row, ch + 1) : piece(row + step, 0);
         bar_sync(kMaxima, kPair);
         if (more && !lost) start(now);  // the chunk is in registers
-        constexpr int kRegs = Sh::kGroups / 32 <= 16 ? Sh::kGroups / 32 : 0;
-        const uint32_t key = a.k > 0 ? keys_bound<kRegs>(groups, Sh::kGroups, a.k) : 0u;
-        // (a search ends early, so a later one may find less)
-        t = ch > 0 ? fmaxf(t, bound_value<T>(key, a.k)) : bound_value<T>(key, a.k);
-        if (lane == 0) bound_sh = part_t[turn] = t;
+        constexpr int kRegs = Sh::kGroups / 32 <= 28 ? Sh::kGroups / 32 : 0;
+        if (a.k > 0) key = keys_bound<kRegs>(groups, Sh::kGroups, a.k, ch > 0 ? key : 0u);
+        const float t = bound_value<T>(key, a.k);
+        // (without its last chunks a row has no bound)
+        if (lane == 0) {
+          bound_sh = t;
+          part_t[turn] = lost ? __int_as_float(0x7FFFFFFF) : t;
+        }
         __syncwarp();
         if (ch == 0) {
           // the list is free again once the last row's candidates are out of it
@@ -947,8 +1068,8 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       float dropped = kNegInf, dropped_s = 0.0f;
       int n = room + 1;
       if (slots <= cap)
-        n = chunks > 1 ? warp_candidates<T, true>(hits, slots, t, found, at, room, dropped)
-                       : warp_candidates<T, false>(hits, slots, t, found, at, room, dropped);
+        n = chunks > 1 ? warp_candidates_again<T>(hits, slots, t, found, at, room, dropped)
+                       : warp_candidates<T>(hits, slots, t, found, at, room);
       const float mw = lane <= kWorkers ? part_m[turn][lane] : kNegInf;
       const float sw = lane <= kWorkers ? part_s[turn][lane] : 0.0f;
       const float m = fmaxf(warp_max(mw), dropped), ref = finite_ref(m);
@@ -960,6 +1081,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       if (n > room) {
         if (lane == 0) {
           a.counts[row] = -1;
+          if (a.k > 0) a.values[row * a.k] = t;
           again = 1;
         }
         __syncwarp();
@@ -975,10 +1097,16 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   }
   __syncthreads();
   if (!again) return;
+  // (what the CTA's shared memory holds, less its buckets)
+  const int all = (int)((topk_smem(Sh::kCap, Sh::kGroups, cap, room, PACK) / 4 - kBuckets) / 4);
   for (int64_t row = blockIdx.x; row < rows; row += step) {
     const int n = a.counts[row];
+    const float t = n == -1 && a.k > 0 ? a.values[row * a.k] : 0.0f;
     __syncthreads();
-    if (n == -1) plain_row<T>(a, row, scan, red);
+    if (n != -1) continue;
+    if (a.k == 0 || t != t ||
+        !again_row<T>(a, row, t, reinterpret_cast<uint32_t*>(smem), all & ~3, &count, red))
+      plain_row<T>(a, row, scan, red);
     __syncthreads();
   }
 }
@@ -1175,12 +1303,12 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
     if (k > 0 && k <= kLaneGroups) {
       // a lane is a group: one key per lane
       const uint32_t own = group_key(most);
-      bound = warp_bound([&](auto f) { f(own); }, k, k + k / 4 + 2);
+      bound = warp_bound([&](auto f) { f(own, 0); }, k, k + k / 4 + 2);
     } else if (k > 0) {
       bound = warp_bound(
           [&](auto f) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) f(top[v]);
+            for (int v = 0; v < NV; ++v) f(top[v], v);
           },
           k, k + k / 4 + 4);
     }
@@ -1312,7 +1440,12 @@ StreamPlan plan_stream(const TopkArgs& a) {
   // first chunk's elements, as many of the second's, which is held against the
   // first's bound, half as many of the third's, and so on; of all those the
   // first number lies above the last bound
-  const int64_t groups = slots < Sh::kGroups ? slots : Sh::kGroups;
+  int64_t groups = p.per;
+  if (groups > Sh::kLanes) {  // (of a chunk that does not fill the buffer, full ones)
+    groups = p.per / (NV / GPT);
+    if (groups < Sh::kLanes) groups = Sh::kLanes;
+    if (groups > Sh::kGroups) groups = Sh::kGroups;
+  }
   const double c = 1.125 * a.k + 4;
   int64_t cap = a.vocab, room = a.vocab;
   if (c < 0.8 * (double)groups) {
@@ -1371,14 +1504,15 @@ void launch_typed(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   else if (slots <= TopkShape<4, 1, 8, 8>::kCap && a.k <= 128)
     launch_stream<T, 4, 1, 8, 8>(a, rows, sms, s);
   else if (slots <= TopkShape<8, 1, 8, 8>::kCap) launch_stream<T, 8, 1, 8, 8>(a, rows, sms, s);
-  else if (a.k <= 256) {
-    // two CTAs per SM where there are rows for them, if need be with less room
-    // (1024 rows of 131071 fp16 logits, k 256: 150 us, else 199)
-    if (rows > sms && resident(1, 2, plan_stream<T, 16, 2, 10, 1>(a).smem, 2) < 2)
-      launch_stream<T, 16, 1, 8, 2>(a, rows, sms, s);
-    else
-      launch_stream<T, 16, 2, 10, 1>(a, rows, sms, s);
-  }
+  // less of a row at once where that lets two CTAs have an SM (1024 rows of
+  // 131071 fp16 logits, k 256: 117 us, else 199); finer groups for larger k
+  else if (a.k <= 256 && rows > sms &&
+           resident(1, 2, plan_stream<T, 16, 2, 10, 1>(a).smem, 2) < 2)
+    launch_stream<T, 16, 2, 8, 2>(a, rows, sms, s);
+  else if (a.k <= 256) launch_stream<T, 16, 2, 10, 1>(a, rows, sms, s);
+  // (1024 rows of 30522 bf16 logits, k 300: 57 us, with ten groups per thread 81;
+  // k 512: 180 and 126)
+  else if (a.k <= 384) launch_stream<T, 16, 2, 10, 2>(a, rows, sms, s);
   else launch_stream<T, 16, 2, 10, 10>(a, rows, sms, s);
 }
 

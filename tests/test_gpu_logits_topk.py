@@ -166,3 +166,28 @@ def test_on_another_stream():
         got = run(y, 64, 2.0)
     side.synchronize()
     assert torch.equal(got[1], want[1]) and torch.equal(got[0], want[0] * 2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab,k", [(70001, 64), (131071, 1024), (150000, 300), (70001, 400)])
+def test_rows_in_several_chunks(dtype, vocab, k):
+    # in any order, ascending (every chunk above all before it), descending, and
+    # the largest few in the last chunk
+    x = logits(5, vocab, k, dtype)
+    x[1] = x[1].sort().values
+    x[2] = x[2].sort(descending=True).values
+    x[3, vocab - 2000:] += 20.0
+    x[4, :vocab // 2] = -math.inf
+    check(x, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab,k", [(130, 70), (1000, 500), (4076, 310), (9000, 300), (70001, 80)])
+def test_as_many_nan_as_the_packet_holds(dtype, vocab, k):
+    x = logits(4, vocab, vocab + k, dtype)
+    x[0] = math.nan
+    x[1, torch.randperm(vocab, generator=_gen(3), device=DEV)[:k]] = math.nan
+    x[2] = -math.inf
+    x[2, ::3] = math.nan
+    x[3, :k] = math.inf
+    check(x, k)
