@@ -113,62 +113,114 @@ __device__ __forceinline__ Part join(const Part& p, int width, float c) {
   return r;
 }
 
-// The row's statistics from all of its parts; `write` stores loss and stats.
-// Everything waits for this, so its steps are few: powers and logarithms by
-// the special-function unit, and none of one taken where a sum will do.  (With
+// log2 of a sum of at least about 1: the whole part and the rest, whose error is
+// that of a logarithm on [0.75, 1.5) however large the sum.
+struct Log2 {
+  float whole, rest;
+  __device__ __forceinline__ float get() const { return whole + rest; }
+};
+template <bool EXACT>
+__device__ __forceinline__ Log2 log2_split(float x) {
+  const int bits = __float_as_int(x), e = (bits - 0x3F400000) >> 23;
+  const float m = __int_as_float(bits - (e << 23));
+  const float rest = EXACT ? log2f(m) : log2_fast(m);
+  return Log2{(float)e, x <= 3.402823466e38f ? rest : x};  // (Inf and NaN stay)
+}
+
+// A row's sums against common references: the student's against its largest
+// logit, the teacher's against 2^rt of its; and the powers in them.
+struct Sums {
+  float sum_s, sum_t, off, tail_e, scale_t, scale_s;
+  float rt, tail2, shift, p_off;
+  bool has_off, none_t;
+};
+
+// What the gradient needs from all of the row's parts.  Every thread of the row
+// waits for this, so its steps are few: powers and logarithms by the
+// special-function unit, and none of one taken where a sum will do.  (With
 // expf, logf and exact divisions the step on 4096 rows of 30522 bf16 logits
 // took 160 us.)
 __device__ __forceinline__ Row finish_row(const Part& p, const DistillArgs& a, float w,
-                                          float row_tail, float* loss_out, float* stats_out) {
+                                          float row_tail, Sums& q) {
   const float c = a.c;
   Row r;
   r.ref = finite_ref(p.m_off);
   r.k2 = 0.0f;
   r.top = finite_ref(fmaxf(p.m_off, p.m_s));
   r.top_t = finite_ref(p.m_t);
-  const bool has_off = p.s_off != 0.0f;
-  const float tail =  // relative to top_t
-      a.tail && has_off ? fmaf(-r.top_t, a.inv_tau, row_tail) : kNegInf;
-  const float tail2 = tail * (1.0f / kLn2);
+  q.has_off = p.s_off != 0.0f;
+  q.tail2 =  // relative to top_t
+      a.tail && q.has_off ? fmaf(-r.top_t, a.inv_tau, row_tail) * (1.0f / kLn2) : kNegInf;
   // reference of the teacher's sum: its largest term
-  const float rt = finite_ref(fmaxf(p.m_t == kNegInf ? kNegInf : 0.0f, tail2));
-  const float shift = finite_ref(p.m_s) - r.top;
-  const float scale_s = p.m_s == kNegInf ? 0.0f : exp2_fast(shift * c);
+  q.rt = finite_ref(fmaxf(p.m_t == kNegInf ? kNegInf : 0.0f, q.tail2));
+  q.shift = finite_ref(p.m_s) - r.top;
+  q.scale_s = p.m_s == kNegInf ? 0.0f : exp2_fast(q.shift * c);
   const float scale_o = exp2_fast((r.ref - r.top) * c);
-  const float scale_t = exp2_fast(-rt), tail_e = exp2_fast(tail2 - rt);
-  const float off = has_off ? p.s_off * scale_o : 0.0f;
-  const float sum_s = fmaf(p.s_s, scale_s, off);
-  const float sum_t = fmaf(p.s_t, scale_t, tail_e);
-  const bool none_t = sum_t == 0.0f;
-  r.log_s = sum_s != 0.0f ? log2_fast(sum_s) : kNegInf;
-  r.log_t = none_t ? kNegInf : rt + log2_fast(sum_t);
-  const float p_off = none_t ? 0.0f : __fdividef(tail_e, sum_t);
+  q.tail_e = exp2_fast(q.tail2 - q.rt);
+  q.scale_t = exp2_fast(-q.rt);
+  q.off = q.has_off ? p.s_off * scale_o : 0.0f;
+  q.sum_s = fmaf(p.s_s, q.scale_s, q.off);
+  q.sum_t = fmaf(p.s_t, q.scale_t, q.tail_e);
+  q.none_t = q.sum_t == 0.0f;
+  r.log_s = q.sum_s != 0.0f ? log2_split<false>(q.sum_s).get() : kNegInf;
+  r.log_t = q.none_t ? kNegInf : q.rt + log2_split<false>(q.sum_t).get();
+  q.p_off = q.none_t ? 0.0f : __fdividef(q.tail_e, q.sum_t);
   r.w = w;
-  r.dead = w == 0.0f || none_t;
+  r.dead = w == 0.0f || q.none_t;
   // a NaN in either log-sum-exp shows in every entry
   r.poison = 0.0f * (r.log_t + r.log_s);
   // w (q_off - p_off) / s_off
-  r.coef = (has_off ? w * (__fdividef(scale_o, sum_s) - __fdividef(p_off, p.s_off)) : 0.0f) +
+  r.coef = (q.has_off ? w * (__fdividef(scale_o, q.sum_s) - __fdividef(q.p_off, p.s_off)) : 0.0f) +
            r.poison;
-  if (loss_out) {
-    // sum_On p (log p - log q) + p_off (log p_off - log q_off); all p add up to 1
-    // and (t - top_t) - (s - top) = (t - top_t) - (s - m_s) - shift
-    const float u = p.s_t != 0.0f ? fmaf(-shift, p.s_t * kUnit, p.u) * scale_t : 0.0f;
-    const float l_off =
-        has_off ? fmaf(r.ref - r.top, a.inv_tau, log2_fast(p.s_off) * kLn2) : kNegInf;
-    float loss = fmaf(r.log_s - r.log_t, kLn2, __fdividef(u, sum_t) * (a.inv_tau / kUnit));
-    if (p_off != 0.0f) loss += p_off * (tail - l_off);
-    *loss_out = none_t ? 0.0f : loss;
-    if (stats_out) {
-      stats_out[0] = r.top;
-      stats_out[1] = l_off;
-      stats_out[2] = r.log_s * kLn2;
-      stats_out[3] = r.top_t;
-      stats_out[4] = r.log_t * kLn2;
-      stats_out[5] = p_off;
-    }
-  }
   return r;
+}
+
+// The row's loss and statistics, by one warp; nobody waits for it.
+//   loss = sum_On p (log p - log q) + p_off (log p_off - log q_off)
+// where, over tau, log p = t - m_t + log scale_t - log sum_t, log q alike.  A loss
+// near 0 is a difference of logarithms of sums of thousands of terms.  So their
+// whole parts are kept apart and cancel exactly, each pair stands beside the
+// probability it counts with, and the logarithms are those of the very powers in
+// the sums: an error in one then moves p or q a little, which a loss near its
+// minimum does not feel.  (As differences of numbers of some 10, losses of 0.02
+// had errors of 3e-6.)
+__device__ __forceinline__ void row_loss(const Part& p, const DistillArgs& a, const Row& r,
+                                         const Sums& q, float* loss_out, float* stats_out) {
+  const int lane = (int)lane_id();
+  float x = q.sum_s, small = 0.0f;  // a power that is next to nothing: its exponent
+  if (lane == 1) x = q.sum_t;
+  if (lane == 2) x = q.off, small = fmaf(r.ref - r.top, a.c, log2_fast(p.s_off));
+  if (lane == 3) x = q.tail_e, small = q.tail2 - q.rt;
+  if (lane == 4) x = q.scale_t, small = -q.rt;
+  if (lane == 5) x = q.scale_s, small = q.shift * a.c;
+  const Log2 one = x < 0x1p-100f ? Log2{0.0f, small} : log2_split<true>(x);
+  const auto of = [&](int from) {
+    return Log2{__shfl_sync(kFull, one.whole, from), __shfl_sync(kFull, one.rest, from)};
+  };
+  const Log2 ls = of(0), lt = of(1), lo = of(2), le = of(3), kt = of(4), ks = of(5);
+  if (lane != 0) return;
+  const float p_on = __fdividef(p.s_t * q.scale_t, q.sum_t);
+  float loss = 0.0f;
+  if (p_on != 0.0f) {
+    loss = __fdividef(p.u * q.scale_t, q.sum_t) * (a.inv_tau / kUnit);
+    const float d = (ls.whole - lt.whole) + (kt.whole - ks.whole) +
+                    ((ls.rest - lt.rest) + (kt.rest - ks.rest));
+    loss = fmaf(p_on, d * kLn2, loss);
+  }
+  if (q.p_off != 0.0f) {
+    const float d = (le.whole - lt.whole) - (lo.whole - ls.whole) +
+                    ((le.rest - lt.rest) - (lo.rest - ls.rest));
+    loss = fmaf(q.p_off, d * kLn2, loss);
+  }
+  *loss_out = q.none_t ? 0.0f : loss + r.poison;
+  if (stats_out) {
+    stats_out[0] = r.top;
+    stats_out[1] = q.has_off ? lo.get() * kLn2 : kNegInf;
+    stats_out[2] = r.log_s * kLn2;
+    stats_out[3] = r.top_t;
+    stats_out[4] = r.log_t * kLn2;
+    stats_out[5] = q.p_off;
+  }
 }
 
 // The same from stored statistics.
@@ -370,9 +422,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     float* v = reinterpret_cast<float*>(&p) + q;
     *v = __shfl_sync(kFull, *v, 0);
   }
-  const bool write = rank == 0 && tid == 0;
-  const Row r = finish_row(p, a, w, a.tail ? a.tail[row] : 0.0f, write ? a.loss + row : nullptr,
-                           write && a.stats ? a.stats + row * 6 : nullptr);
+  const float tail = a.tail ? a.tail[row] : 0.0f;
+  Sums sums;
+  const Row r = finish_row(p, a, w, tail, sums);
+  if (rank == 0 && warp == 0)
+    row_loss(p, a, r, sums, a.loss + row, a.stats ? a.stats + row * 6 : nullptr);
   if (!GRAD) {
     if (cluster > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     return;
@@ -692,8 +746,9 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
 
   const float nan = __int_as_float(0x7FFFFFFF);
   // joins the warps' sums (one pair per lane) with the packet's, and the
-  // cluster's, and writes the row's loss
-  const auto conclude = [&](const Next& me, Part all, float mw, float sw, bool bad, float w) {
+  // cluster's
+  const auto conclude = [&](const Next& me, Part& all, Sums& sums, float mw, float sw, bool bad,
+                            float w) {
     all.m_off = warp_max(mw);
     all.s_off = warp_sum(sw * rescale(mw, all.m_off, c));
     if (cluster > 1 && !bad) {
@@ -719,19 +774,24 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       side ^= 1;
       bad = lost;
     }
-    const bool write = me.rank == 0 && lane == 0;
-    Row r = finish_row(all, a, w, me.tail, write ? a.loss + me.row : nullptr,
-                       write && a.stats ? a.stats + me.row * 6 : nullptr);
+    Row r = finish_row(all, a, w, me.tail, sums);
     if (bad) {
       r.coef = r.poison = nan;
       r.dead = w == 0.0f;
-      if (write) {
-        a.loss[me.row] = nan;
-        if (a.stats)
-          for (int q = 0; q < 6; ++q) a.stats[me.row * 6 + q] = nan;
-      }
     }
     return r;
+  };
+  const auto write_loss = [&](const Next& me, const Part& all, const Row& r, const Sums& sums,
+                              bool bad) {
+    if (me.rank != 0) return;
+    float* stats = a.stats ? a.stats + me.row * 6 : nullptr;
+    if (!bad) {
+      row_loss(all, a, r, sums, a.loss + me.row, stats);
+    } else if (lane == 0) {
+      a.loss[me.row] = nan;
+      if (stats)
+        for (int q = 0; q < 6; ++q) stats[q] = nan;
+    }
   };
 
   if (first >= items) {
@@ -742,14 +802,11 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
   start_copy(me);
   start_packet(me, 0);
   prepare(me, 0);
-  // the row before: its gradient (GRAD), or all of its end (loss alone: nobody
-  // waits for it, so it is concluded while the others read the next row)
+  // the row before, whose gradient is not finished
   Next last;
   Row last_r;
-  Part last_on;
-  float last_m = kNegInf, last_s = 0.0f, last_end = 0.0f;
+  float last_end = 0.0f;
   int last_n = 0;
-  bool last_bad = false;
   for (int64_t item = first; item < items; item += step, turn ^= 1) {
     if (!LOSS) {
       Row r = stored_row(a, me.row, w);
@@ -803,15 +860,18 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
       const float m_end = warp_max(end);
       const float s_end = warp_sum(exp2_fast((end - finite_ref(m_end)) * c));
       bar_sync(kParts, kThreads);
-      last_m = lane < kWorkers ? part_m[lane] : lane == kWorkers ? m_end : kNegInf;
-      last_s = lane < kWorkers ? part_s[lane] : lane == kWorkers ? s_end : 0.0f;
-      last_r = conclude(me, on, last_m, last_s, bad, w);
+      const float mw = lane < kWorkers ? part_m[lane] : lane == kWorkers ? m_end : kNegInf;
+      const float sw = lane < kWorkers ? part_s[lane] : lane == kWorkers ? s_end : 0.0f;
+      Sums sums;
+      last_r = conclude(me, on, sums, mw, sw, bad, w);
       bad |= lost;
       if (GRAD) {
         if (lane == 0) row_sh[turn] = last_r;
         __syncwarp();
         bar_sync(kRowDone, kThreads);
       }
+      write_loss(me, on, last_r, sums, bad);
+      __syncwarp();
     }
     last = me;
     last_n = bad ? 0 : n;
@@ -1018,8 +1078,10 @@ __global__ void __launch_bounds__(kRingWarps * 32, 4)
     last.m_off = warp_max(mw);
     last.s_off = warp_sum(mw == kNegInf ? sw : sw * rescale(mw, last.m_off, c));
     const bool bad = last_bad || lost;
-    finish_row(last, a, 0.0f, last_tail, lane == 0 && !bad ? a.loss + open : nullptr,
-               a.stats ? a.stats + open * 6 : nullptr);
+    Sums sums;
+    const Row r = finish_row(last, a, 0.0f, last_tail, sums);
+    if (!bad)
+      row_loss(last, a, r, sums, a.loss + open, a.stats ? a.stats + open * 6 : nullptr);
     if (bad && lane == 0) {
       a.loss[open] = nan;
       if (a.stats)
@@ -1312,9 +1374,9 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
         p.s_t = warp_sum(p.s_t);
         p.u = warp_sum(p.u);
       }
-      float* loss_out = me.rank == 0 && lane == 0 ? a.loss + me.row : nullptr;
-      float* stats_out = me.rank == 0 && lane == 0 && a.stats ? a.stats + me.row * 6 : nullptr;
-      r = finish_row(p, a, w, me.tail, loss_out, stats_out);
+      Sums sums;
+      r = finish_row(p, a, w, me.tail, sums);
+      row_loss(p, a, r, sums, a.loss + me.row, a.stats ? a.stats + me.row * 6 : nullptr);
     } else {
       r = stored_row(a, me.row, w);
     }

@@ -362,3 +362,26 @@ def test_argument_errors():
     with pytest.raises(efg.EFError):                       # a part of the logits
         efg.distill_loss_grad(s[:, :50], val, idx, 1.0, loss,
                               s.view(-1)[10:110].view(2, 50))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab,k,tau", [
+    (6, 200, 5, 1.0), (40, 2000, 64, 2.0), (7, 30522, 64, 2.0), (3, 131071, 1, 2.15),
+    (320, 40000, 100, 1.0)])
+def test_losses_near_zero_keep_their_digits(dtype, rows, vocab, k, tau):
+    # a student that is the teacher: the loss is 0 but for the powers' errors, at
+    # most 2^-22 of a term on either side of the packet, and those of six
+    # logarithms between 1/2 and 2, a unit in the last place each
+    x = torch.randn(rows, vocab, generator=torch.Generator(device="cuda").manual_seed(k),
+                    device="cuda").to(dtype) * 2
+    v, i = torch.empty(rows, k, device="cuda"), torch.empty(rows, k, dtype=torch.int32,
+                                                            device="cuda")
+    c, tail = torch.empty(rows, dtype=torch.int32, device="cuda"), torch.empty(rows,
+                                                                               device="cuda")
+    efg.logits_topk(x, k, tau, v, i, c, tail)
+    loss = torch.empty(rows, device="cuda")
+    efg.distill_loss(x, v, i, tau, loss, counts=c, tail=tail)
+    assert float(loss.abs().max()) <= 2 * 2.0 ** -22 + 6 * 2.0 ** -23
+    grad, again = torch.empty_like(x), torch.empty(rows, device="cuda")
+    efg.distill_loss_grad(x, v, i, tau, again, grad, counts=c, tail=tail)
+    assert float(again.abs().max()) <= 2 * 2.0 ** -22 + 6 * 2.0 ** -23
