@@ -14,11 +14,16 @@
 // exchanged within the group.  The next token's logits are loaded before the
 // current one is worked on.
 //
-// Segments of a few rounds of tokens are finished by one cluster of CTAs each,
-// in one launch.  Longer ones are cut into tiles over the whole
+// Segments that are short, or many and alike, are finished by one cluster of CTAs
+// each, in one launch.  Longer ones are cut into tiles over the whole
 // device: zero, count (shared-memory histograms, added to the counts with
 // integer atomics), then the pass, whose last CTA adds the tiles' sums in tile
 // order.
+//
+// Loss and gradient of 131072 tokens, 256 fp32 experts, k 8: 61 us, of which
+// zeroing and counting take 9 and wait for nothing but launches and atomics; the
+// pass over the logits runs at 5.8 TB/s.  32768 tokens of 64 bf16 experts in 64
+// segments, loss alone: 8.7 us.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -35,9 +40,13 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCountThreads = 1024;
 constexpr int kSegBatch = 512;  // segments per launch
 constexpr float kLog2e = 1.4426950408889634f;
-// Rounds of eight CTAs' warps up to which one launch with a cluster per segment
-// beats the launches over the device.
-constexpr int64_t kOneLaunch = 12;
+// Elements per lane that a cluster of eight CTAs goes through for the longest
+// segment, up to which one launch with a cluster per segment beats the launches
+// over the device, where few segments leave SMs idle.  (One segment of 64 bf16
+// experts, loss and gradient, 2048 tokens, 64 elements: 8.0 us against 10.1, 4096:
+// 10.7 against 10.1; 256 fp32 experts, 512 tokens, 64 elements: 9.5 against 11.1,
+// 1024: 14.4 against 10.9.)
+constexpr int64_t kOneLaunch = 96;
 
 struct SegBatch {
   int32_t n;                   // segments
@@ -558,7 +567,10 @@ ef_status launch_batch(BalanceArgs a, const SegBatch& seg, int first, int sms, c
   if constexpr (LOSS) {
     // rounds of a CTA's warps over the longest segment, on a cluster of eight
     const int64_t round = kWarps * (32 / form.G);
-    if (longest <= kOneLaunch * 8 * round) {
+    const int64_t each = form.wide ? form.nv * (16 / (int)sizeof(T)) : form.nv;
+    // or segments enough, and alike enough, to fill the device (64 of 2048 tokens,
+    // 256 fp32 experts: 58 us against 67; of 8192, 64 bf16 experts: 34 against 43)
+    if (longest * each <= kOneLaunch * 8 * round || 8 * tokens >= longest * 3 * sms) {
       // CTAs per segment: one round each, while that leaves SMs idle
       int cluster = 1;
       while (cluster < 8 && longest > cluster * round && seg.n * cluster < 4 * sms) cluster *= 2;
