@@ -1017,8 +1017,11 @@ def run_case(args):
     'topk_2p20' (the 2^20-element top-1 % step with its receive side), 'sign'
     (1-bit compression of 4 workers' gradients of n elements, then their
     sign aggregate with G and SGD), 'q8' (top-0.1 % with 8-bit values, then
-    the receiver's dequantisation) or 'codec' (a top-0.1 % packet of n
-    elements encoded and decoded with each index codec)."""
+    the receiver's dequantisation), 'codec' (a top-0.1 % packet of n
+    elements encoded and decoded with each index codec) or 'losses' (row
+    packets of n / 30522 rows of 30522 bf16 logits, the distillation loss and
+    gradient against them, and the balance loss and gradient of 4 n / 30522
+    tokens over 256 experts)."""
     import torch
     import error_feedback_gradient_gb300 as efg
     from error_feedback_gradient_gb300 import workloads as wl
@@ -1107,6 +1110,27 @@ def run_case(args):
         for _ in range(3):
             efg.topk_compress_q8(g, e, [0, n], [k], q, sc, ix, None, ws)
             efg.q8_dequantize(q, sc, [k], v)
+    elif args.case == "losses":
+        rows, vocab, k = max(1, n // 30522), 30522, 64
+        x = wl.normal(rows * vocab, 3.0, 1, dev).view(rows, vocab).to(torch.bfloat16)
+        v = torch.empty(rows, k, device=dev)
+        ix = torch.empty(rows, k, dtype=torch.int32, device=dev)
+        cnt = torch.empty(rows, dtype=torch.int32, device=dev)
+        tail, loss = torch.empty(rows, device=dev), torch.empty(rows, device=dev)
+        grad = torch.empty_like(x)
+        tokens, experts = 4 * rows, 256
+        z = wl.normal(tokens * experts, 1.0, 2, dev).view(tokens, experts)
+        ids = torch.topk(z, 8, dim=1).indices.to(torch.int32)
+        bal, used = torch.empty(1, device=dev), torch.empty(1, dtype=torch.int32, device=dev)
+        table = torch.empty(1, experts, dtype=torch.int32, device=dev)
+        gz = torch.empty_like(z)
+        ws = torch.empty(efg.balance_workspace_size(tokens, experts, 8, [0, tokens]),
+                         dtype=torch.uint8, device=dev)
+        for _ in range(3):
+            efg.logits_topk(x, k, 2.0, v, ix, cnt, tail)
+            efg.distill_loss_grad(x, v, ix, 2.0, loss, grad, counts=cnt, tail=tail)
+            efg.balance_loss_grad(z, ids, [0, tokens], 0.01, 0.001, bal, table, used, gz,
+                                  workspace=ws)
     else:
         g = wl.student_t3(n, 1e-3, 1, dev)
         e = torch.zeros_like(g)
@@ -1126,7 +1150,7 @@ def run_case(args):
                 if not torch.equal(back, ix):
                     raise SystemExit(f"codec {codec}: round trip differs")
     torch.cuda.synchronize()
-    status = 0 if args.case == "sign" else efg.workspace_status(ws)
+    status = 0 if args.case in ("sign", "losses") else efg.workspace_status(ws)
     print(json.dumps({"case": args.case, "n": n, "k": k, "status": status}))
 
 
@@ -1157,7 +1181,7 @@ def main(argv=None):
                    help="time the exchanged step instead: one worker per rank, top-k, "
                         "packet exchange across the ranks, receive side")
     p.add_argument("--case", choices=["topk", "aggregate", "randk", "resnet50", "topk_2p20",
-                                       "sign", "q8", "codec"],
+                                       "sign", "q8", "codec", "losses"],
                    default=None,
                    help="run one entry point alone (three calls at --n) for profiling")
     args = p.parse_args(argv)

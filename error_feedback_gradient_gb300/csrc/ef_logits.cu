@@ -1119,7 +1119,10 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS)
 
 constexpr int kShortWarps = 4;  // per CTA
 // Up to this k the 32 lanes' maxima bound it well (12 of 32: some 15 candidates),
-// and each step of the search is one comparison instead of one per slot.
+// and each step of the search is one comparison instead of one per slot (16384
+// rows of 1000 fp32 logits, k 10: 31 us, from slot maxima 34; k 16: 36 and 35).
+// What bounds these rows is the number of instructions, 1370 per row: issue slots
+// are 58 % and the integer pipe 55 % busy.
 constexpr int kLaneGroups = 12;
 
 __host__ __device__ constexpr size_t short_smem(int slots, int cap) {
