@@ -479,13 +479,15 @@ EF_API ef_status sign_aggregate_apply(int32_t W, const uint32_t* const* h_bits,
  *              -0 equal to +0; a logit of -Inf is never taken
  *   count    = |S|  (less than k only where the row has fewer entries > -Inf)
  *   values   = x[v], indices = v for v in S, ascending; unused slots 0 and -1
+ *              (a -0 comes back as +0, every NaN as the same one)
  *   tail     = log sum_{v not in S} exp(x[v] / tau), -Inf for an empty sum
  * With k = 0 the tail is the log-sum-exp of the whole row.
  *
  * out_values  [rows][k] fp32, out_indices [rows][k] int32 (may be NULL for
  *             k = 0); out_counts [rows] int32; out_tail [rows] fp32 or NULL.
  * Outputs must not overlap logits or each other.
- * Device status: none can arise; the call takes no workspace.
+ * Device status: none; the call takes no workspace.  Rows that a bounded wait
+ * inside the kernel has run out on are read again by a path without waits.
  * ---------------------------------------------------------------------- */
 EF_API ef_status ef_logits_topk(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                 int64_t row_stride, int32_t k, float tau, float* out_values,
@@ -535,7 +537,8 @@ EF_API ef_status ef_logits_topk(const void* logits, int32_t dtype, int64_t rows,
  *                  Only its first `vocab` elements per row are written.
  * Device status: none; the calls take no workspace.  A packet whose indices
  * are not strictly ascending in [0, vocab) is never followed out of bounds:
- * its row's loss, stats and gradient are NaN.
+ * its row's loss, stats and gradient are NaN, as are those of rows on which a
+ * bounded wait inside the kernel has run out.
  * ---------------------------------------------------------------------- */
 EF_API ef_status ef_distill_loss(const void* logits, int32_t dtype, int64_t rows, int64_t vocab,
                                  int64_t row_stride, int32_t k, const float* values,
