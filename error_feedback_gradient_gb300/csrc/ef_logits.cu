@@ -1419,6 +1419,9 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8)
     }
 }
 
+// Dynamic shared memory that needs no attribute: 48 KB less the kernels' own.
+constexpr size_t kPlainSmem = 46 * 1024;
+
 // CTAs of a persistent kernel: as many as fit the device, at most `most`.
 int64_t resident(int sms, int by_threads, size_t smem, int64_t most) {
   int fit = (int)(225 * 1024 / (smem + 2048));
@@ -1473,7 +1476,7 @@ template <typename T, int WARPS, int PACK, int NV, int GPT>
 void launch_stream(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   const auto kernel = topk_stream<T, WARPS, PACK, NV, GPT>;
   const StreamPlan p = plan_stream<T, WARPS, PACK, NV, GPT>(a);
-  if (p.smem > 48 * 1024)
+  if (p.smem > kPlainSmem)
     (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   const int64_t grid = resident(sms, 32 / WARPS, p.smem, rows);
   launch_pdl(kernel, dim3((unsigned)grid), dim3(WARPS * 32), p.smem, s, a, rows, p.chunks, p.per,
@@ -1490,7 +1493,7 @@ void launch_short(const TopkArgs& a, int64_t rows, int sms, cudaStream_t s) {
   cap = (cap + 3) & ~3;
   const size_t smem = kShortWarps * short_smem(32 * NV, (int)cap);
   const auto kernel = topk_short<T, NV>;
-  if (smem > 48 * 1024)
+  if (smem > kPlainSmem)
     (void)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   const int64_t grid = resident(sms, 8, smem, (rows + kShortWarps - 1) / kShortWarps);
   launch_pdl(kernel, dim3((unsigned)grid), dim3(kShortWarps * 32), smem, s, a, rows, (int)cap);

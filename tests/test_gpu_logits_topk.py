@@ -191,3 +191,14 @@ def test_as_many_nan_as_the_packet_holds(dtype, vocab, k):
     x[2, ::3] = math.nan
     x[3, :k] = math.inf
     check(x, k)
+
+
+@pytest.mark.parametrize("dtype,vocabs", [(torch.float32, range(960, 1040, 3)),
+                                          (torch.float32, range(448, 520, 5)),
+                                          (torch.bfloat16, range(960, 1040, 7)),
+                                          (torch.float16, range(1980, 2060, 7))])
+def test_candidates_lists_of_every_size(dtype, vocabs):
+    # shared memory from a little below to a little above what a launch gets unasked
+    for vocab in vocabs:
+        for k in (60, 97, 130, 250):
+            check(logits(2, vocab, vocab + k, dtype), k)
